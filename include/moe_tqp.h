@@ -123,7 +123,9 @@ typedef enum {
   MOE_CALL_PERMUTE = 1,
   MOE_CALL_EXPERT_FWD = 2,
   MOE_CALL_COMBINE = 3,
-  MOE_CALL_ADAPTER_BWD = 4
+  MOE_CALL_ADAPTER_BWD = 4,
+  MOE_CALL_BALANCE_FWD = 5,
+  MOE_CALL_ROUTER_BWD = 6
 } moe_call;
 
 /* Flags OR-ed into the call id of moe_workspace_size: what the caller will
@@ -399,6 +401,144 @@ typedef struct {
 moe_status moe_adamw_step(const moe_adamw_hparams *h, int64_t n, float *master,
                           const float *grad, float *m, float *v, void *param,
                           int32_t param_dtype, void *stream);
+
+/* Load-balance loss of a routed batch, with the per-expert counts, and its
+ * gradient with respect to the router logits.  Routing over many experts
+ * collapses onto few unless something holds the loads together ("Reversible
+ * Sparse MoE Single Node" skill card, Principle 2 and its routing-collapse
+ * check); the pages give no loss, and this is the product of the loads and
+ * the mean probabilities over the experts:
+ *   p_t = softmax(logits[t]) over all E experts, n = tokens that take part,
+ *   counts[e] = #{(t, j): topk_idx[t][j] = e}, prob[e] = (1/n) sum_t p_t[e],
+ *   loss = E sum_e counts[e] / (n k) prob[e]     (1 when the loads are even),
+ *   dlogits[t][e] = p_t[e] (w[e] - sum_i w[i] p_t[i]),
+ *   w[e] = dloss[0] E counts[e] / (n^2 k)        (the counts held fixed).
+ * float32, the sums over tokens in a fixed order and ended in double.
+ * moe_balance_bwd takes n and the counts from `counts`: when a batch is split
+ * over processes, adding `counts` over them between the two calls gives the
+ * gradient with the whole batch's loads.
+ *   logits    f32 [T][E], as moe_route writes them
+ *   topk_idx  i32 [T][k]; an entry outside [0, E) is counted nowhere
+ *   valid     u8 [T] or NULL (every token): 0 marks a token that takes no
+ *             part.  Nothing of its row is read: its logits may hold anything,
+ *             it is not counted, its row of dlogits is 0
+ *   loss      f32 [1] (out)
+ *   counts    i32 [E+1] (out): slots per expert, then n
+ *   prob      f32 [E] (out)
+ *   stats     f32 [T][2] (out), 8-byte aligned: the largest logit and the sum
+ *             of exp(logit - largest) of each row; (0, 0) for a token without
+ *             a part
+ *   dloss     f32 [1]: gradient of the loss (device)
+ *   dlogits   f32 [T][E] (out); may be the logits themselves
+ * A logit of -inf has probability 0; a row that is -inf throughout adds
+ * nothing to prob and has gradient 0 (it counts in n).  NaN and +inf give NaN.
+ * With n = 0 the loss, prob and the gradient are 0.
+ *   ws        moe_workspace_size(MOE_CALL_BALANCE_FWD) bytes, 16-byte aligned */
+moe_status moe_balance_fwd(const moe_dims *dims, const float *logits, const int32_t *topk_idx,
+                           const uint8_t *valid, float *loss, int32_t *counts, float *prob,
+                           float *stats, void *ws, size_t ws_bytes, void *stream);
+moe_status moe_balance_bwd(const moe_dims *dims, const float *logits, const float *stats,
+                           const int32_t *counts, const uint8_t *valid, const float *dloss,
+                           float *dlogits, void *stream);
+
+/* Gradient of the gates with respect to the router logits, added to
+ * dlogits_in.  moe_adapter_bwd carries this gradient into dx and leaves the
+ * router frozen; a caller that trains the full-precision router (skill card
+ * "Reversible Sparse MoE Single Node", Implementation Considerations, TQP
+ * Quantization) takes it from here to moe_router_bwd.  With e_j, g_j, p_j the
+ * experts, gates and slot positions of token t:
+ *   dgamma_j = <dy_t, e_out[p_j]>, dsel_j = g_j (dgamma_j - sum_i g_i dgamma_i),
+ *   dlogits[t][e] = dlogits_in[t][e] + sum_{j: e_j = e} dsel_j
+ * in float32.
+ *   dy          act [T][d], e_out act [S][d] (permuted order): 16-byte aligned
+ *   topk_idx, gates, slot_pos  as written by moe_route and moe_permute
+ *               (indices outside their range are clamped into it)
+ *   valid       u8 [T] or NULL; the row of a token marked 0 is set to 0 and
+ *               nothing of that token is read
+ *   dlogits_in  f32 [T][E] or NULL (0), e.g. from moe_balance_bwd
+ *   dlogits     f32 [T][E] (out); may be dlogits_in */
+moe_status moe_gate_bwd(const moe_dims *dims, const void *dy, const void *e_out,
+                        const int32_t *topk_idx, const float *gates, const int32_t *slot_pos,
+                        const uint8_t *valid, const float *dlogits_in, float *dlogits,
+                        void *stream);
+
+/* Backward of the router's product logits = x W_r + b for a logit gradient
+ * D = dlogits:
+ *   dx = dx_in + D W_r^T, dw_router[c][e] = sum_t x[t][c] D[t][e],
+ *   db_router[e] = sum_t D[t][e].
+ * The dx of moe_adapter_bwd already holds the gates' share, so a training
+ * step takes dx from the balance loss's gradient (dx_in = that dx) and the
+ * weight gradients from the sum that moe_gate_bwd writes.  dw_router and
+ * db_router have the router's layouts, ready for moe_adamw_step.  Products
+ * and sums keep float32 accuracy; dx is rounded to act once.
+ *   x          act [T][d], 16-byte aligned; read only for dw_router
+ *   w_router   f32 [d][E]; read only for dx
+ *   valid      u8 [T] or NULL; a token marked 0 takes no part: its rows of x
+ *              and dlogits are not read, its row of dx is that of dx_in (or 0)
+ *   dlogits    f32 [T][E]
+ *   dx_in      act [T][d] or NULL (0), 16-byte aligned
+ *   dx         act [T][d] (out) or NULL, 16-byte aligned; may be dx_in
+ *   dw_router  f32 [d][E] (out) or NULL;  db_router f32 [E] (out) or NULL
+ *   ws         moe_workspace_size(MOE_CALL_ROUTER_BWD) bytes, 16-byte aligned */
+moe_status moe_router_bwd(const moe_dims *dims, const void *x, const float *w_router,
+                          const uint8_t *valid, const float *dlogits, const void *dx_in, void *dx,
+                          float *dw_router, float *db_router, void *ws, size_t ws_bytes,
+                          void *stream);
+
+/* Rows quantized to int8 with a scale per row, for moe_i8_linear.  For every
+ * row p < M (with offsets: p < offsets[E], the rows behind stay as they were):
+ *   v = x[p]                              plain,
+ *   v = silu(x[p]) mul[p]                 mul given (silu(z) = z / (1 + e^-z)),
+ *   v times col_scale[e] per column       col_scale given, e the row's expert,
+ *   scale[p] = max|v| / 127,  q[p][c] = v / scale[p] rounded to nearest (ties
+ *   to even, as if from the exact quotient), in [-127, 127].
+ * v and scale are float32.  A row of zeros has scale 0 and q 0; a row with a
+ * value that is not finite has scale NaN and q 0.
+ *   act        moe_dtype of x and mul
+ *   x, mul     act [M][K] with row strides ldx, ldm >= K (elements)
+ *   col_scale  f32 [E][K] or NULL
+ *   offsets    i32 [E+1] as written by moe_permute, or NULL (then E = 1)
+ *   q          int8 [M][ldq] (out), 16-byte aligned; ldq a multiple of 16, at
+ *              least K rounded up to 128; columns K .. ldq-1 are set to 0
+ *   scale      f32 [M] (out)
+ * Limits: 0 <= M <= 2^26 (0 enqueues nothing), 1 <= K <= 65536, E <= 1024. */
+moe_status moe_quant_i8(int32_t M, int32_t K, int32_t act, const void *x, int64_t ldx,
+                        const void *mul, int64_t ldm, const float *col_scale,
+                        const int32_t *offsets, int32_t n_experts, int8_t *q, int64_t ldq,
+                        float *scale, void *stream);
+
+/* Product of int8 rows with int8 matrices, a scale per row and per output
+ * channel (the "Int8" base of the skill card "Reversible Sparse MoE Single
+ * Node", TQP Quantization, with one scale per output channel in the place of
+ * moe_qlora's groups, and rows in 8 bits).  For rows p with offsets[e] <= p <
+ * offsets[e+1], r = row_src ? row_src[p] / row_div : p:
+ *   out[p][n] = a_scale[r] w_scale[e][n] sum_k a[r][k] w[e][n][k],
+ * the sum exact in int32, the scales applied in float32, one rounding to act.
+ * Rows behind offsets[E] stay as they were.  The gradient of the rows is the
+ * same product: rows of dout quantized by moe_quant_i8 with col_scale =
+ * w_scale, the matrices transposed to [E][K][N], w_scale NULL.
+ *   a        int8 [a_rows][lda], 16-byte aligned, as moe_quant_i8 writes it:
+ *            lda a multiple of 16, at least K rounded up to 128, columns from
+ *            K on 0
+ *   a_scale  f32 [a_rows]
+ *   row_src  i32 [M] or NULL (then a_rows >= M); moe_permute's perm_src with
+ *            row_div = top_k reads the rows by token (indices outside a are
+ *            clamped into it)
+ *   offsets  i32 [E+1] or NULL (every row, E = 1)
+ *   w        int8 [E][N][ldw], 16-byte aligned, in -128 .. 127; ldw a multiple
+ *            of 16, at least K (what stands behind column K is not used)
+ *   w_scale  f32 [E][N] or NULL (1)
+ *   out      act [M][ldo] (out), ldo >= N; must not overlap the inputs
+ * Limits: 0 <= M <= 2^26 (0 enqueues nothing), N, K in [1, 65536], E <= 1024,
+ * strides <= 2^20. */
+typedef struct {
+  int32_t M, N, K, n_experts;
+  int32_t act;        /* moe_dtype of out */
+} moe_i8_dims;
+moe_status moe_i8_linear(const moe_i8_dims *dims, const int8_t *a, int64_t lda,
+                         const float *a_scale, int32_t a_rows, const int32_t *row_src,
+                         int32_t row_div, const int32_t *offsets, const int8_t *w, int64_t ldw,
+                         const float *w_scale, void *out, int64_t ldo, void *stream);
 
 /* Instrumentation, not part of the method: time every launch of one internal
  * kernel with a pair of HIP events recorded on the launch stream around it.

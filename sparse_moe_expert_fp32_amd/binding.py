@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_tqp.
 
 MOE_F32, MOE_BF16 = 0, 1
 CALL_ROUTE, CALL_PERMUTE, CALL_EXPERT_FWD, CALL_COMBINE, CALL_ADAPTER_BWD = range(5)
+CALL_BALANCE_FWD, CALL_ROUTER_BWD = 5, 6
 # workspace flags OR-ed into a call id of moe_workspace_size
 WS_SAVE_GIVEN, WS_PACKED_GIVEN = 0x100, 0x200
 MAT_GATE_UP, MAT_DOWN = 0, 1
@@ -38,6 +39,11 @@ class QLora(ctypes.Structure):
                 ("qf", ctypes.c_void_p)]
 
 
+class I8Dims(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("n_experts", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
 class AdamWHparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float),
@@ -50,6 +56,7 @@ def _load():
                        "`python -m sparse_moe_expert_fp32_amd.build`")
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    I64 = ctypes.c_int64
     DP = ctypes.POINTER(Dims)
     sig = {
         "moe_route": [DP, P, P, P, P, P, P, P, SZ, P],
@@ -72,6 +79,13 @@ def _load():
         "moe_pack_base_f_size": [DP, ctypes.POINTER(SZ)],
         "moe_pack_base_f": [DP, I32, P, P, P, SZ, P],
         "moe_rev_couple": [DP, P, P, P, I32, P],
+        "moe_balance_fwd": [DP, P, P, P, P, P, P, P, P, SZ, P],
+        "moe_balance_bwd": [DP, P, P, P, P, P, P, P],
+        "moe_gate_bwd": [DP, P, P, P, P, P, P, P, P, P],
+        "moe_router_bwd": [DP, P, P, P, P, P, P, P, P, P, SZ, P],
+        "moe_quant_i8": [I32, I32, I32, P, I64, P, I64, P, P, I32, P, I64, P, P],
+        "moe_i8_linear": [ctypes.POINTER(I8Dims), P, I64, P, I32, P, I32, P, P, I64, P, P, I64,
+                          P],
         "moe_grow_copy": [P, P, ctypes.c_int64, I32, I32, P],
         "moe_grow_router": [I32, I32, I32, P, P, P, ctypes.c_float, P, P, P],
     }
@@ -90,7 +104,8 @@ EXPORTS = ("moe_route", "moe_permute", "moe_expert_fwd", "moe_expert_fwd_noalloc
            "moe_workspace_size", "moe_save_size", "moe_status_string", "moe_last_error",
            "moe_abi_version", "moe_timer_start", "moe_timer_stop", "moe_adamw_step",
            "moe_pack_base_t_size", "moe_pack_base_t", "moe_pack_base_f_size", "moe_pack_base_f",
-           "moe_rev_couple", "moe_grow_copy", "moe_grow_router")
+           "moe_rev_couple", "moe_grow_copy", "moe_grow_router", "moe_balance_fwd",
+           "moe_balance_bwd", "moe_gate_bwd", "moe_router_bwd", "moe_quant_i8", "moe_i8_linear")
 
 # kernel tags of moe_timer_start (moe_kernel_tag)
 KT = {"router_logits": 0, "router_topk": 1, "permute": 2, "gateup": 3, "down": 4, "combine": 5,
@@ -257,3 +272,187 @@ def moe_adamw_step(h: AdamWHparams, master, grad, m, v, param=None, stream=None)
     n = master.numel()
     _check(LIB.moe_adamw_step(ctypes.byref(h), n, _p(master), _p(grad), _p(m), _p(v), _p(param),
                               pdt, _stream(stream)), "moe_adamw_step")
+
+
+# ---- load balance, router training, int8 rows and products.  The tensors'
+# types, sizes and layouts are checked here (the C ABI sees pointers only),
+# and the call runs with the tensors' device current.
+
+_F32, _I32, _I8 = torch.float32, torch.int32, torch.int8
+_ACT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _need(ok, name, what):
+    if not ok:
+        raise MoeError(f"{name}: {what}")
+
+
+def _dense(name, arg, t, dtypes, numel, dev):
+    """One contiguous device tensor of `numel` elements of one of `dtypes`."""
+    if t.dtype not in dtypes or t.numel() != numel or t.device != dev or not t.is_contiguous():
+        raise MoeError(f"{name}: {arg} must be a contiguous {'/'.join(str(d) for d in dtypes)} "
+                       f"tensor of {numel} elements on {dev}, got {t.dtype} {tuple(t.shape)} "
+                       f"on {t.device}")
+
+
+def _checked(name, dev, *specs):
+    if dev.type != "cuda":
+        raise MoeError(f"{name}: tensors must be on the GPU, got {dev}")
+    for arg, t, dtypes, numel in specs:
+        if t is not None:
+            _dense(name, arg, t, dtypes, numel, dev)
+
+
+def _call(name, dev, fn, args, stream):
+    """Call fn(*args, stream) with `dev` current, on its current stream
+    unless one is given."""
+    if dev.index == torch.cuda.current_device():
+        st = _stream(stream)
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(stream))
+    if status:
+        _check(status, name)
+
+
+def _bytes(ws):
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+_BOOLS = (torch.bool, torch.uint8)
+
+
+def moe_balance_fwd(dm: Dims, logits, topk_idx, valid, loss, counts, prob, stats, ws, stream=None):
+    """Load-balance loss, per-expert counts (and the number of tokens, last)
+    and mean probabilities; `stats` is what moe_balance_bwd reads."""
+    T, E, dev = dm.T, dm.n_experts, logits.device
+    _checked("moe_balance_fwd", dev, ("logits", logits, (_F32,), T * E),
+             ("topk_idx", topk_idx, (_I32,), T * dm.top_k), ("valid", valid, _BOOLS, T),
+             ("loss", loss, (_F32,), 1), ("counts", counts, (_I32,), E + 1),
+             ("prob", prob, (_F32,), E), ("stats", stats, (_F32,), 2 * T))
+    _need(ws is None or ws.device == dev, "moe_balance_fwd", "ws is on another device")
+    _call("moe_balance_fwd", dev, LIB.moe_balance_fwd,
+          (ctypes.byref(dm), _p(logits), _p(topk_idx), _p(valid), _p(loss), _p(counts), _p(prob),
+           _p(stats), _p(ws), _bytes(ws)), stream)
+
+
+def moe_balance_bwd(dm: Dims, logits, stats, counts, valid, dloss, dlogits, stream=None):
+    """Gradient of the load-balance loss with respect to the logits."""
+    T, E, dev = dm.T, dm.n_experts, logits.device
+    _checked("moe_balance_bwd", dev, ("logits", logits, (_F32,), T * E),
+             ("stats", stats, (_F32,), 2 * T), ("counts", counts, (_I32,), E + 1),
+             ("valid", valid, _BOOLS, T), ("dloss", dloss, (_F32,), 1),
+             ("dlogits", dlogits, (_F32,), T * E))
+    _call("moe_balance_bwd", dev, LIB.moe_balance_bwd,
+          (ctypes.byref(dm), _p(logits), _p(stats), _p(counts), _p(valid), _p(dloss),
+           _p(dlogits)), stream)
+
+
+def _act_of(dm):
+    return (torch.bfloat16,) if dm.act == MOE_BF16 else (torch.float32,)
+
+
+def moe_gate_bwd(dm: Dims, dy, e_out, topk_idx, gates, slot_pos, valid, dlogits_in, dlogits,
+                 stream=None):
+    """dlogits = dlogits_in + the gates' gradient with respect to the logits."""
+    T, E, k, d, dev = dm.T, dm.n_experts, dm.top_k, dm.d_model, dy.device
+    _checked("moe_gate_bwd", dev, ("dy", dy, _act_of(dm), T * d),
+             ("e_out", e_out, _act_of(dm), T * k * d), ("topk_idx", topk_idx, (_I32,), T * k),
+             ("gates", gates, (_F32,), T * k), ("slot_pos", slot_pos, (_I32,), T * k),
+             ("valid", valid, _BOOLS, T), ("dlogits_in", dlogits_in, (_F32,), T * E),
+             ("dlogits", dlogits, (_F32,), T * E))
+    _call("moe_gate_bwd", dev, LIB.moe_gate_bwd,
+          (ctypes.byref(dm), _p(dy), _p(e_out), _p(topk_idx), _p(gates), _p(slot_pos), _p(valid),
+           _p(dlogits_in), _p(dlogits)), stream)
+
+
+def moe_router_bwd(dm: Dims, x, w_router, valid, dlogits, dx_in, dx, dw_router, db_router, ws,
+                   stream=None):
+    """dx = dx_in + dlogits W_r^T, dw_router = x^T dlogits, db_router = the
+    column sums of dlogits; each output may be None."""
+    T, E, d, dev = dm.T, dm.n_experts, dm.d_model, dlogits.device
+    _checked("moe_router_bwd", dev, ("x", x, _act_of(dm), T * d),
+             ("w_router", w_router, (_F32,), d * E), ("valid", valid, _BOOLS, T),
+             ("dlogits", dlogits, (_F32,), T * E), ("dx_in", dx_in, _act_of(dm), T * d),
+             ("dx", dx, _act_of(dm), T * d), ("dw_router", dw_router, (_F32,), d * E),
+             ("db_router", db_router, (_F32,), E))
+    _need(ws is None or ws.device == dev, "moe_router_bwd", "ws is on another device")
+    _call("moe_router_bwd", dev, LIB.moe_router_bwd,
+          (ctypes.byref(dm), _p(x), _p(w_router), _p(valid), _p(dlogits), _p(dx_in), _p(dx),
+           _p(dw_router), _p(db_router), _p(ws), _bytes(ws)), stream)
+
+
+def moe_i8_stride(K: int) -> int:
+    """Row stride of int8 rows of K values (moe_quant_i8, moe_i8_linear)."""
+    return (K + 127) // 128 * 128
+
+
+def _rows(name, arg, t, dtypes, dev):
+    """(rows, columns, row stride) of a matrix whose columns are adjacent."""
+    if t.dim() != 2 or t.dtype not in dtypes or t.device != dev or \
+            (t.stride(1) != 1 and t.shape[1] > 1):
+        raise MoeError(f"{name}: {arg} must be a {'/'.join(str(d) for d in dtypes)} matrix on "
+                       f"{dev} with adjacent columns, got {t.dtype} {tuple(t.shape)} "
+                       f"{t.stride()} on {t.device}")
+    M, N = t.shape
+    return M, N, t.stride(0) if M > 1 else max(t.stride(0), N)
+
+
+def _experts(name, offsets, E, dev):
+    if offsets is not None:
+        _dense(name, "offsets", offsets, (_I32,), E + 1, dev)
+
+
+def moe_quant_i8(x, q, scale, mul=None, col_scale=None, offsets=None, stream=None):
+    """Rows of x (or silu(x) mul, or x col_scale[expert]) -> int8 rows q
+    [M][moe_i8_stride(K)] and their scales [M]."""
+    name, dev = "moe_quant_i8", x.device
+    _need(dev.type == "cuda", name, f"tensors must be on the GPU, got {dev}")
+    M, K, ldx = _rows(name, "x", x, tuple(_ACT), dev)
+    Mq, Kq, ldq = _rows(name, "q", q, (_I8,), dev)
+    _need(Mq == M and Kq >= moe_i8_stride(K), name,
+          f"q must have {M} rows of at least {moe_i8_stride(K)} values, got {tuple(q.shape)}")
+    _dense(name, "scale", scale, (_F32,), M, dev)
+    ldm, E = 0, 1
+    if mul is not None:
+        Mm, Km, ldm = _rows(name, "mul", mul, (x.dtype,), dev)
+        _need((Mm, Km) == (M, K), name, f"mul must be {(M, K)}, got {tuple(mul.shape)}")
+    if offsets is not None:
+        E = offsets.numel() - 1
+        _experts(name, offsets, E, dev)
+    if col_scale is not None:
+        _dense(name, "col_scale", col_scale, (_F32,), E * K, dev)
+    _call(name, dev, LIB.moe_quant_i8,
+          (M, K, _ACT[x.dtype], _p(x), ldx, _p(mul), ldm, _p(col_scale), _p(offsets), E, _p(q),
+           ldq, _p(scale)), stream)
+
+
+def moe_i8_linear(a, a_scale, w, w_scale, out, offsets=None, row_src=None, row_div=1,
+                  stream=None):
+    """out[p] = rows a (int8, as moe_quant_i8 writes them) by the int8 matrix
+    w[e] [N][K] of the row's expert, scaled per row and per channel."""
+    name, dev = "moe_i8_linear", a.device
+    _need(dev.type == "cuda", name, f"tensors must be on the GPU, got {dev}")
+    R, Ka, lda = _rows(name, "a", a, (_I8,), dev)
+    M, N, ldo = _rows(name, "out", out, tuple(_ACT), dev)
+    _need(w.dim() == 3 and w.dtype in (_I8, torch.uint8) and w.device == dev and
+          w.shape[1] == N and (w.stride(2) == 1 or w.shape[2] == 1), name,
+          f"w must be int8 [E][{N}][K] with adjacent columns on {dev}, got {w.dtype} "
+          f"{tuple(w.shape)} {w.stride()} on {w.device}")
+    E, _, K = w.shape
+    ldw = w.stride(1) if N > 1 else (w.stride(0) if E > 1 else max(w.stride(1), K))
+    _need(E == 1 or w.stride(0) == N * ldw, name, "the experts' matrices must lie one after another")
+    _need(w.untyped_storage().nbytes() - w.storage_offset() >= E * N * ldw, name,
+          "the last row of w must reach its stride")
+    _need(Ka >= moe_i8_stride(K), name, f"a must have rows of at least {moe_i8_stride(K)} values")
+    _dense(name, "a_scale", a_scale, (_F32,), R, dev)
+    if w_scale is not None:
+        _dense(name, "w_scale", w_scale, (_F32,), E * N, dev)
+    if row_src is not None:
+        _dense(name, "row_src", row_src, (_I32,), M, dev)
+    _experts(name, offsets, E, dev)
+    d = I8Dims(M, N, K, E, _ACT[out.dtype])
+    _call(name, dev, LIB.moe_i8_linear,
+          (ctypes.byref(d), _p(a), lda, _p(a_scale), R, _p(row_src), row_div, _p(offsets), _p(w),
+           ldw, _p(w_scale), _p(out), ldo), stream)

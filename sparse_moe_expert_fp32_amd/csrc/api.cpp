@@ -244,6 +244,8 @@ size_t ws_bytes_for(const moe_dims *d, int call) {
     case MOE_CALL_EXPERT_FWD: return FwdLayout(d, flags).total;
     case MOE_CALL_COMBINE: return 0;
     case MOE_CALL_ADAPTER_BWD: return BwdLayout(d, flags).total;
+    case MOE_CALL_BALANCE_FWD: return moe::balance_ws_bytes(d->T, d->n_experts);
+    case MOE_CALL_ROUTER_BWD: return moe::router_bwd_ws_bytes(d->T, d->d_model, d->n_experts);
     default: return (size_t)-1;
   }
 }
@@ -264,6 +266,9 @@ moe_status check_ws(const moe_dims *d, int call, const void *ws, size_t ws_bytes
                                        " bytes, got " + std::to_string(ws_bytes));
   return MOE_OK;
 }
+
+// row stride of int8 rows: the products read them in 128-byte steps
+int64_t i8_stride(int K) { return ((int64_t)K + 127) & ~int64_t(127); }
 
 template <typename T> T *at(void *base, size_t off) { return (T *)((char *)base + off); }
 
@@ -362,7 +367,7 @@ moe_status moe_workspace_size(const moe_dims *dims, int32_t call, size_t *bytes)
   TRY(check_dims(dims));
   if (!bytes) return fail(MOE_ERR_INVALID, "bytes is NULL");
   const int id = call & 0xff, flags = call & ~0xff;
-  if (id < MOE_CALL_ROUTE || id > MOE_CALL_ADAPTER_BWD)
+  if (id < MOE_CALL_ROUTE || id > MOE_CALL_ROUTER_BWD)
     return fail(MOE_ERR_INVALID, "unknown call id");
   if (flags & ~(MOE_WS_SAVE_GIVEN | MOE_WS_PACKED_GIVEN))
     return fail(MOE_ERR_INVALID, "unknown workspace flag");
@@ -1048,6 +1053,130 @@ moe_status moe_adapter_bwd(const moe_dims *dims, const void *dy, const void *x,
   TIMED(MOE_KT_BWD_GATEUP, st, moe::launch_lin_simple(bf, true, A, st));
   moe::launch_unpermute_sum(bf, true, dx_r, dXp, slot_pos, T, d, k, dx, st);
   return hip_status("moe_adapter_bwd");
+}
+
+// ---- load balance and router training
+
+moe_status moe_balance_fwd(const moe_dims *dims, const float *logits, const int32_t *topk_idx,
+                           const uint8_t *valid, float *loss, int32_t *counts, float *prob,
+                           float *stats, void *ws, size_t ws_bytes, void *stream) {
+  TRY(check_dims(dims));
+  REQUIRE(logits && topk_idx && loss && counts && prob && stats,
+          "moe_balance_fwd: logits, topk_idx, loss, counts, prob and stats required");
+  REQUIRE(((uintptr_t)stats & 7) == 0, "moe_balance_fwd: stats must be 8-byte aligned");
+  TRY(check_ws(dims, MOE_CALL_BALANCE_FWD, ws, ws_bytes));
+  REQUIRE(((uintptr_t)ws & 15) == 0, "moe_balance_fwd: ws must be 16-byte aligned");
+  moe::launch_balance_fwd(logits, topk_idx, valid, dims->T, dims->n_experts, dims->top_k, loss,
+                          counts, prob, stats, ws, (hipStream_t)stream);
+  return hip_status("moe_balance_fwd");
+}
+
+moe_status moe_balance_bwd(const moe_dims *dims, const float *logits, const float *stats,
+                           const int32_t *counts, const uint8_t *valid, const float *dloss,
+                           float *dlogits, void *stream) {
+  TRY(check_dims(dims));
+  REQUIRE(logits && stats && counts && dloss && dlogits,
+          "moe_balance_bwd: logits, stats, counts, dloss and dlogits required");
+  REQUIRE(((uintptr_t)stats & 7) == 0, "moe_balance_bwd: stats must be 8-byte aligned");
+  moe::launch_balance_bwd(logits, stats, counts, valid, dloss, dims->T, dims->n_experts,
+                          dims->top_k, dlogits, (hipStream_t)stream);
+  return hip_status("moe_balance_bwd");
+}
+
+moe_status moe_gate_bwd(const moe_dims *dims, const void *dy, const void *e_out,
+                        const int32_t *topk_idx, const float *gates, const int32_t *slot_pos,
+                        const uint8_t *valid, const float *dlogits_in, float *dlogits,
+                        void *stream) {
+  TRY(check_dims(dims));
+  REQUIRE(dy && e_out && topk_idx && gates && slot_pos && dlogits,
+          "moe_gate_bwd: dy, e_out, topk_idx, gates, slot_pos and dlogits required");
+  REQUIRE((((uintptr_t)dy | (uintptr_t)e_out) & 15) == 0,
+          "moe_gate_bwd: dy and e_out must be 16-byte aligned");
+  moe::launch_gate_bwd(dims->act == MOE_BF16, dy, e_out, topk_idx, gates, slot_pos, valid,
+                       dlogits_in, dims->T, dims->d_model, dims->n_experts, dims->top_k, dlogits,
+                       (hipStream_t)stream);
+  return hip_status("moe_gate_bwd");
+}
+
+moe_status moe_router_bwd(const moe_dims *dims, const void *x, const float *w_router,
+                          const uint8_t *valid, const float *dlogits, const void *dx_in, void *dx,
+                          float *dw_router, float *db_router, void *ws, size_t ws_bytes,
+                          void *stream) {
+  TRY(check_dims(dims));
+  REQUIRE(dlogits, "moe_router_bwd: dlogits required");
+  REQUIRE(dx || dw_router || db_router,
+          "moe_router_bwd: at least one of dx, dw_router and db_router required");
+  REQUIRE(!dx || w_router, "moe_router_bwd: w_router required when dx is requested");
+  REQUIRE(dx || !dx_in, "moe_router_bwd: dx_in without dx");
+  REQUIRE(!dw_router || x, "moe_router_bwd: x required when dw_router is requested");
+  REQUIRE((((uintptr_t)x | (uintptr_t)dx_in | (uintptr_t)dx) & 15) == 0,
+          "moe_router_bwd: x, dx_in and dx must be 16-byte aligned");
+  TRY(check_ws(dims, MOE_CALL_ROUTER_BWD, ws, ws_bytes));
+  REQUIRE(((uintptr_t)ws & 15) == 0, "moe_router_bwd: ws must be 16-byte aligned");
+  moe::launch_router_bwd(dims->act == MOE_BF16, x, w_router, valid, dlogits, dx_in, dims->T,
+                         dims->d_model, dims->n_experts, dx, dw_router, db_router, ws,
+                         (hipStream_t)stream);
+  return hip_status("moe_router_bwd");
+}
+
+// ---- int8 rows and products
+
+moe_status moe_quant_i8(int32_t M, int32_t K, int32_t act, const void *x, int64_t ldx,
+                        const void *mul, int64_t ldm, const float *col_scale,
+                        const int32_t *offsets, int32_t n_experts, int8_t *q, int64_t ldq,
+                        float *scale, void *stream) {
+  REQUIRE(M >= 0 && M <= (1 << 26), "moe_quant_i8: M must be in [0, 2^26]");
+  REQUIRE(K >= 1 && K <= 65536, "moe_quant_i8: K must be in [1, 65536]");
+  REQUIRE(n_experts >= 1 && n_experts <= 1024, "moe_quant_i8: n_experts must be in [1, 1024]");
+  if (act != MOE_F32 && act != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_quant_i8: act must be MOE_F32 or MOE_BF16");
+  REQUIRE(ldx >= K && (!mul || ldm >= K), "moe_quant_i8: row strides must be at least K");
+  REQUIRE(ldq >= i8_stride(K) && ldq <= (1 << 20) && ldq % 16 == 0,
+          "moe_quant_i8: ldq must be a multiple of 16, at least K rounded up to 128");
+  REQUIRE(offsets || n_experts == 1, "moe_quant_i8: offsets required for several experts");
+  if (M == 0) return MOE_OK;
+  REQUIRE(x && q && scale, "moe_quant_i8: x, q and scale required");
+  REQUIRE(((uintptr_t)q & 15) == 0, "moe_quant_i8: q must be 16-byte aligned");
+  moe::QuantArgs A{};
+  A.M = M; A.K = K; A.E = n_experts;
+  A.x = x; A.ldx = ldx; A.u = mul; A.ldu = ldm;
+  A.col_scale = col_scale; A.offsets = offsets;
+  A.q = q; A.ldq = ldq; A.scale = scale;
+  moe::launch_quant_i8(act == MOE_BF16, A, (hipStream_t)stream);
+  return hip_status("moe_quant_i8");
+}
+
+moe_status moe_i8_linear(const moe_i8_dims *dims, const int8_t *a, int64_t lda,
+                         const float *a_scale, int32_t a_rows, const int32_t *row_src,
+                         int32_t row_div, const int32_t *offsets, const int8_t *w, int64_t ldw,
+                         const float *w_scale, void *out, int64_t ldo, void *stream) {
+  REQUIRE(dims, "moe_i8_linear: dims is NULL");
+  REQUIRE(dims->M >= 0 && dims->M <= (1 << 26), "moe_i8_linear: M must be in [0, 2^26]");
+  REQUIRE(dims->N >= 1 && dims->N <= 65536, "moe_i8_linear: N must be in [1, 65536]");
+  REQUIRE(dims->K >= 1 && dims->K <= 65536, "moe_i8_linear: K must be in [1, 65536]");
+  REQUIRE(dims->n_experts >= 1 && dims->n_experts <= 1024,
+          "moe_i8_linear: n_experts must be in [1, 1024]");
+  if (dims->act != MOE_F32 && dims->act != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_i8_linear: act must be MOE_F32 or MOE_BF16");
+  REQUIRE(lda % 16 == 0 && lda >= i8_stride(dims->K) && lda <= (1 << 20),
+          "moe_i8_linear: lda must be a multiple of 16, at least K rounded up to 128");
+  REQUIRE(ldw % 16 == 0 && ldw >= dims->K && ldw <= (1 << 20),
+          "moe_i8_linear: ldw must be a multiple of 16, at least K");
+  REQUIRE(ldo >= dims->N && ldo <= (1 << 20), "moe_i8_linear: ldo must be at least N");
+  REQUIRE(a_rows >= 0 && a_rows <= (1 << 26), "moe_i8_linear: a_rows must be in [0, 2^26]");
+  REQUIRE(!row_src || row_div >= 1, "moe_i8_linear: row_div must be at least 1");
+  REQUIRE(offsets || dims->n_experts == 1, "moe_i8_linear: offsets required for several experts");
+  if (dims->M == 0) return MOE_OK;
+  REQUIRE(a_rows >= (row_src ? 1 : dims->M), "moe_i8_linear: fewer rows in a than the product reads");
+  REQUIRE(a && a_scale && w && out, "moe_i8_linear: a, a_scale, w and out required");
+  REQUIRE((((uintptr_t)a | (uintptr_t)w) & 15) == 0, "moe_i8_linear: a and w must be 16-byte aligned");
+  moe::LinearI8Args A{};
+  A.M = dims->M; A.N = dims->N; A.K = dims->K; A.E = dims->n_experts;
+  A.a = a; A.lda = lda; A.a_scale = a_scale; A.a_rows = a_rows;
+  A.row_src = row_src; A.row_div = row_div; A.offsets = offsets;
+  A.w = w; A.ldw = ldw; A.w_scale = w_scale; A.out = out; A.ldo = ldo;
+  moe::launch_linear_i8(dims->act == MOE_BF16, A, (hipStream_t)stream);
+  return hip_status("moe_i8_linear");
 }
 
 }  // extern "C"

@@ -290,4 +290,44 @@ struct AdamWArgs {
 // out_kind: 0 none, 1 float32 copy, 2 bf16 copy
 void launch_adamw(const AdamWArgs &h, int out_kind, hipStream_t st);
 
+// ---- load-balance loss (balance.hip)
+constexpr int ceil_div_h(int a, int b) { return (a + b - 1) / b; }
+size_t balance_ws_bytes(int T, int E);
+void launch_balance_fwd(const float *logits, const int32_t *topk_idx, const uint8_t *valid, int T,
+                        int E, int k, float *loss, int32_t *counts, float *prob, float *stats,
+                        void *ws, hipStream_t st);
+void launch_balance_bwd(const float *logits, const float *stats, const int32_t *counts,
+                        const uint8_t *valid, const float *dloss, int T, int E, int k,
+                        float *dlogits, hipStream_t st);
+
+// ---- backward of the router (router_bwd.hip)
+void launch_gate_bwd(bool bf16, const void *dy, const void *e_out, const int32_t *topk_idx,
+                     const float *gates, const int32_t *slot_pos, const uint8_t *valid,
+                     const float *dl_in, int T, int d, int E, int k, float *dl_out,
+                     hipStream_t st);
+size_t router_bwd_ws_bytes(int T, int d, int E);
+// dx, dw and db may each be null
+void launch_router_bwd(bool bf16, const void *x, const float *w, const uint8_t *valid,
+                       const float *dl, const void *dx_in, int T, int d, int E, void *dx,
+                       float *dw, float *db, void *ws, hipStream_t st);
+
+// ---- int8 rows and products (quant_i8.hip, linear_i8.hip)
+struct QuantArgs {
+  int M, K, E;
+  const void *x, *u; int64_t ldx, ldu;       // u: SwiGLU of x and u, or null
+  const float *col_scale;                    // [E][K] or null
+  const int32_t *offsets;                    // [E + 1] or null (every row of expert 0)
+  int8_t *q; int64_t ldq; float *scale;
+};
+void launch_quant_i8(bool bf16, const QuantArgs &A, hipStream_t st);
+struct LinearI8Args {
+  int M, N, K, E;
+  const int8_t *a; int64_t lda; const float *a_scale; int a_rows;
+  const int32_t *row_src; int row_div;
+  const int32_t *offsets;
+  const int8_t *w; int64_t ldw; const float *w_scale;
+  void *out; int64_t ldo;
+};
+void launch_linear_i8(bool bf16, const LinearI8Args &A, hipStream_t st);
+
 }  // namespace moe

@@ -140,6 +140,50 @@ class DeviceLayer:
         self.forward(stream)
         B.moe_rev_couple(self.dm, y2, self.y, x2, -1, stream)
 
+    # ---- router training: load-balance loss and the router's own gradients
+    def init_router_training(self):
+        """Buffers of the load-balance loss and the router's gradients (the
+        layer needs want_logits=True and a backward)."""
+        if self.logits is None or self.save is None:
+            raise ValueError("router training needs want_logits=True and a layer with a backward")
+        cfg, new = self.cfg, lambda *n, dt=torch.float32: torch.empty(n, dtype=dt, device=self.dev)
+        self.bal_loss, self.bal_counts = new(1), new(cfg.E + 1, dt=torch.int32)
+        self.bal_prob, self.bal_stats = new(cfg.E), new(cfg.T, 2)
+        self.bal_dloss = new(1)
+        self.dlogits_bal, self.dlogits = new(cfg.T, cfg.E), new(cfg.T, cfg.E)
+        self.dw_router = new(cfg.d, cfg.E)
+        self.db_router = new(cfg.E) if self.t.get("b_router") is not None else None
+        for c in (B.CALL_BALANCE_FWD, B.CALL_ROUTER_BWD):
+            self.ws[c] = torch.empty(max(1, B.moe_workspace_size(self.dm, c)), dtype=torch.uint8,
+                                     device=self.dev)
+
+    def balance(self, valid=None, stream=None):
+        """Load-balance loss and counts of the routed batch (after route())."""
+        B.moe_balance_fwd(self.dm, self.logits, self.topk_idx, valid, self.bal_loss,
+                          self.bal_counts, self.bal_prob, self.bal_stats,
+                          self.ws[B.CALL_BALANCE_FWD], stream)
+
+    def router_bwd(self, valid=None, stream=None):
+        """Gradients of the router (after adapter_bwd() and balance(), with
+        bal_dloss set): the balance loss's share is added to dx, and
+        dw_router, db_router hold the gates' and the balance loss's share."""
+        t = self.t
+        B.moe_balance_bwd(self.dm, self.logits, self.bal_stats, self.bal_counts, valid,
+                          self.bal_dloss, self.dlogits_bal, stream)
+        B.moe_router_bwd(self.dm, t["x"], t["w_router"], valid, self.dlogits_bal, self.dx, self.dx,
+                         None, None, self.ws[B.CALL_ROUTER_BWD], stream)
+        B.moe_gate_bwd(self.dm, t["dy"], self.e_out, self.topk_idx, self.gates, self.slot_pos,
+                       valid, self.dlogits_bal, self.dlogits, stream)
+        B.moe_router_bwd(self.dm, t["x"], t["w_router"], valid, self.dlogits, None, None,
+                         self.dw_router, self.db_router, self.ws[B.CALL_ROUTER_BWD], stream)
+
+    def router_train_step(self, valid=None, stream=None):
+        """train_step() with the load-balance loss and the router's gradients."""
+        self.forward(stream)
+        self.balance(valid, stream)
+        self.adapter_bwd(stream)
+        self.router_bwd(valid, stream)
+
     # ---- adapter optimizer (AdamW through moe_adamw_step)
     ADAPTERS = (("dA_gate", "A_gate"), ("dB_gate", "B_gate"), ("dA_up", "A_up"),
                 ("dB_up", "B_up"), ("dA_down", "A_down"), ("dB_down", "B_down"))
@@ -169,6 +213,65 @@ class DeviceLayer:
         if self.logits is not None:
             out["logits"] = to_numpy(self.logits)
         return out
+
+
+class Int8Experts:
+    """SwiGLU experts with int8 matrices and one scale per output channel:
+    the expert forward in 8-bit integers (rows quantized per token) and the
+    gradient of its products' rows.
+
+    gate_up int8 [E][2f][d] (gate's channels, then up's) with scales [E][2f],
+    down int8 [E][d][f] with scales [E][d], on the GPU."""
+
+    def __init__(self, gate_up, s_gate_up, down, s_down):
+        self.gate_up, self.s_gate_up, self.down, self.s_down = gate_up, s_gate_up, down, s_down
+        self.E, f2, self.d = gate_up.shape
+        self.f = f2 // 2
+        self.t = None
+
+    def _rows(self, M, K):
+        dev = self.down.device
+        return (torch.empty(M, B.moe_i8_stride(K), dtype=torch.int8, device=dev),
+                torch.empty(M, dtype=torch.float32, device=dev))
+
+    def forward(self, L: DeviceLayer, stream=None):
+        """e_out of a routed and permuted layer L from its x."""
+        T, S, f = L.cfg.T, L.cfg.S, self.f
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            raise TypeError("stream must be a torch.cuda.Stream or None")
+        with torch.cuda.stream(stream):
+            q, s = self._rows(T, self.d)
+            gu = torch.empty(S, 2 * f, dtype=L.e_out.dtype, device=L.e_out.device)
+            hq, hs = self._rows(S, f)
+            B.moe_quant_i8(L.t["x"], q, s)
+            B.moe_i8_linear(q, s, self.gate_up, self.s_gate_up, gu, offsets=L.offsets,
+                            row_src=L.perm_src, row_div=L.cfg.k)
+            B.moe_quant_i8(gu[:, :f], hq, hs, mul=gu[:, f:])
+            B.moe_i8_linear(hq, hs, self.down, self.s_down, L.e_out, offsets=L.offsets)
+        return gu
+
+    def transpose(self):
+        """The matrices as the row gradients read them, laid out once (they
+        are frozen); rows padded to 16 bytes."""
+        def turned(w):
+            E, N, K = w.shape
+            room = torch.zeros(E, K, (N + 15) // 16 * 16, dtype=w.dtype, device=w.device)
+            room[:, :, :N] = w.transpose(1, 2)
+            return room[:, :, :N]
+        self.t = {"gate_up": turned(self.gate_up), "down": turned(self.down)}
+
+    def rows_grad(self, which: str, dout, offsets, stream=None):
+        """Gradient of the rows of the product `which` ("gate_up" or "down")
+        for the gradient dout of its output, permuted order."""
+        if self.t is None:
+            self.transpose()
+        w, cs = self.t[which], self.s_gate_up if which == "gate_up" else self.s_down
+        with torch.cuda.stream(stream):
+            q, s = self._rows(*dout.shape)
+            dx = torch.empty(dout.shape[0], w.shape[1], dtype=dout.dtype, device=dout.device)
+            B.moe_quant_i8(dout, q, s, col_scale=cs, offsets=offsets)
+            B.moe_i8_linear(q, s, w, None, dx, offsets=offsets)
+        return dx
 
 
 def grow_inputs(t: dict, cfg, factor: int, noise=None, noise_scale: float = 0.0):

@@ -1,0 +1,460 @@
+"""Int8 rows and products on the GPU against the definition in float64: the
+quantized values and the integer sums are exact, the scales carry counted
+float32 roundings (U = 2^-24) and one rounding to the output type."""
+import numpy as np
+import pytest
+import torch
+
+from sparse_moe_expert_fp32_amd import binding as B, configs, inputs
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DEV = "cuda:0"
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def f64(t):
+    return t.double().cpu()
+
+
+# -------------------------------------------------------------------- rows --
+
+def quant_ref(v):
+    """v float32 [M][K] -> (q, scale): the quotient rounded from 64 bits (a
+    quotient of two float32 numbers never falls on the wrong side of a border
+    there)."""
+    scale = (v.abs().max(1).values.double() / 127).float()
+    s = scale.double()
+    q = torch.where(s[:, None] > 0, torch.round(v.double() / s.clamp_min(1e-300)[:, None]), 0.0)
+    return q.clamp(-127, 127).to(torch.int8), scale
+
+
+def run_quant(x, K, **kw):
+    M = x.shape[0]
+    ld = kw.pop("ldq", B.moe_i8_stride(K))
+    q = torch.full((M, ld), 55, dtype=torch.int8, device=DEV)
+    s = torch.full((M,), -77.0, device=DEV)
+    B.moe_quant_i8(x, q, s, **kw)
+    torch.cuda.synchronize()
+    return q, s
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,K", [(1, 1), (1, 2048), (5, 7), (33, 128), (64, 129), (9, 1000),
+                                 (3, 4096), (2, 5001), (300, 768), (2, 20000)])
+def test_quant_rows(cuda_ok, M, K, dt):
+    x = torch.randn(M, K, generator=gen(M + K)).to(dt)
+    q, s = run_quant(x.to(DEV), K)
+    rq, rs = quant_ref(x.float())
+    assert torch.equal(s.cpu(), rs)
+    assert torch.equal(q.cpu()[:, :K], rq) and torch.all(q[:, K:] == 0)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_quant_ties_and_extremes(cuda_ok, dt):
+    """Quotients that end in one half go to the even side; zeros, subnormal
+    and huge rows, and rows with values that are no numbers."""
+    K = 300
+    x = torch.zeros(12, K)
+    ints = torch.arange(K) % 255 - 127
+    x[0] = ints.float() * 0.5                      # scale 0.5: halves at odd places
+    x[0, 0] = 63.5
+    x[1] = torch.where(torch.arange(K) % 2 == 0, 63.5, -31.75)   # amax / 2, amax / 4
+    x[1, 5] = 127.0
+    x[3] = torch.randn(K, generator=gen(1)) * 1e-39
+    x[4] = torch.randn(K, generator=gen(2)) * 1e-45
+    x[5] = torch.randn(K, generator=gen(3)) * 1e37
+    x[6, 17] = float("nan")
+    x[7] = 1.0
+    x[7, 100] = float("inf")
+    x[8, 3] = -5.0
+    x[9] = torch.randn(K, generator=gen(4)) * 1e-30
+    x[10, :] = torch.finfo(torch.float32).max if dt == torch.float32 else 3e38
+    x[11] = torch.linspace(-1, 1, K)
+    x = x.to(dt)
+    q, s = run_quant(x.to(DEV), K)
+    fine = [i for i in range(12) if i not in (6, 7)]
+    rq, rs = quant_ref(x.float()[fine])
+    assert torch.equal(s.cpu()[fine], rs)
+    assert torch.equal(q.cpu()[fine][:, :K], rq)
+    assert s[2] == 0 and torch.all(q[2] == 0)
+    for i in (6, 7):
+        assert torch.isnan(s[i]) and torch.all(q[i] == 0)
+
+
+def test_quant_strides_and_wider_rows(cuda_ok):
+    """Rows of a wider matrix off a 16-byte boundary, and q wider than needed."""
+    for off in (0, 1, 8):
+        wide = torch.randn(20, 333, generator=gen(off)).bfloat16()
+        x = wide.to(DEV)[:, off:off + 200]
+        q, s = run_quant(x, 200, ldq=272)
+        rq, rs = quant_ref(wide[:, off:off + 200].float())
+        assert torch.equal(s.cpu(), rs) and torch.equal(q.cpu()[:, :200], rq)
+        assert torch.all(q[:, 200:] == 0)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("K", [1, 100, 768, 4100])
+def test_quant_channel_scales_by_expert(cuda_ok, K, dt):
+    """The row's expert picks the multipliers; rows behind the last expert
+    stay as they were."""
+    counts = [0, 3, 0, 1, 7, 0, 5, 0]
+    E, S = len(counts), sum(counts)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32)
+    x = torch.randn(S + 4, K, generator=gen(K)).to(dt)
+    cs = torch.rand(E, K, generator=gen(9)) + 0.1
+    q, s = run_quant(x.to(DEV), K, col_scale=cs.to(DEV), offsets=off.to(DEV))
+    e = torch.repeat_interleave(torch.arange(E), torch.tensor(counts))
+    rq, rs = quant_ref(x[:S].float() * cs[e])       # one float32 product
+    assert torch.equal(s.cpu()[:S], rs) and torch.equal(q.cpu()[:S, :K], rq)
+    assert torch.all(q[S:] == 55) and torch.all(s[S:] == -77)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,K", [(1, 1), (4, 768), (37, 1001), (3, 5000)])
+def test_quant_swiglu(cuda_ok, M, K, dt):
+    gu = (torch.randn(M, 2 * K, generator=gen(M * K)) * 3).to(dt)
+    gu[0, 0] = -200.0                                # exp(200) overflows: silu is 0
+    d = gu.to(DEV)
+    q, s = run_quant(d[:, :K], K, mul=d[:, K:])
+    g, u = gu[:, :K].double(), gu[:, K:].double()
+    v = g * torch.sigmoid(g) * u
+    amax = v.abs().max(1).values
+    # exp, 1 + e, the quotient and the product: at most 8 roundings of v
+    assert torch.all((f64(s) - amax / 127).abs() <= 10 * U * amax / 127 + 1e-44)
+    got = f64(q)[:, :K] * f64(s)[:, None]
+    assert torch.all((got - v).abs() <= f64(s)[:, None] * (0.5 + 127 * 10 * U) + 8 * U * v.abs() + 1e-44)
+    assert torch.all(q[:, K:] == 0)
+
+
+# ---------------------------------------------------------------- products --
+
+def linear_case(counts, N, K, dt, seed, div=1, pad=0, scales=True, src=True):
+    g = gen(seed)
+    E, S = len(counts), sum(counts)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32)
+    R = max(1, (S + div - 1) // div)
+    a = torch.zeros(R, B.moe_i8_stride(K), dtype=torch.int8)
+    a[:, :K] = torch.randint(-127, 128, (R, K), generator=g).to(torch.int8)
+    ldw = (K + 15) // 16 * 16 + 16 * pad
+    w = torch.randint(-128, 128, (E, N, ldw), generator=g).to(torch.int8)   # what stands behind K is not used
+    a_s = torch.rand(R, generator=g) + 0.01
+    w_s = (torch.rand(E, N, generator=g) + 0.01) * 1e-3 if scales else None
+    rows = torch.randint(0, R * div, (S,), generator=g).to(torch.int32) if src else None
+    return off, a, w[:, :, :K], a_s, w_s, rows
+
+
+def linear_ref(off, a, w, a_s, w_s, rows, div):
+    S, K = int(off[-1]), w.shape[2]
+    r = (rows.long() // div) if rows is not None else torch.arange(S)
+    out = torch.zeros(S, w.shape[1], dtype=torch.float64)
+    for e in range(w.shape[0]):
+        i, j = int(off[e]), int(off[e + 1])
+        if j > i:
+            out[i:j] = a[r[i:j], :K].double() @ w[e].double().t()
+            out[i:j] *= a_s[r[i:j]].double()[:, None] * (w_s[e].double() if w_s is not None else 1.0)
+    return out
+
+
+def check_linear(counts, N, K, dt, seed=0, div=1, pad=0, scales=True, src=True, extra=3, wide=5,
+                 no_offsets=False):
+    off, a, w, a_s, w_s, rows = linear_case(counts, N, K, dt, seed, div, pad, scales, src)
+    S = int(off[-1])
+    if no_offsets:
+        extra = 0
+    if not src and S + extra > a.shape[0]:
+        extra = a.shape[0] - S
+    out = torch.full((S + extra, N + wide), -77.0, dtype=dt, device=DEV)
+    to = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    wd = torch.empty(w.shape[0], N, w.stride(1), dtype=torch.int8, device=DEV)
+    wd.copy_(torch.as_strided(w, wd.shape, w.stride()))
+    src_d = None
+    if rows is not None:
+        src_d = torch.zeros(S + extra, dtype=torch.int32)
+        src_d[:S] = rows
+        src_d = src_d.to(DEV)
+    B.moe_i8_linear(to(a), to(a_s), wd[:, :, :K], to(w_s), out[:, :N],
+                    offsets=None if no_offsets else to(off), row_src=src_d, row_div=div)
+    torch.cuda.synchronize()
+    ref = linear_ref(off, a, w, a_s, w_s, rows, div)
+    got = f64(out)
+    # the sum to float32, the product of the scales, their product: 3 roundings
+    tol = ref.abs() * (3.1 * U + HALF[dt] * (1 + 4 * U))
+    bad = (got[:S, :N] - ref).abs() > tol
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4])
+    assert torch.all(got[S:] == -77) and torch.all(got[:, N:] == -77)   # left as it was
+    return out
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1, 1), (1, 2048, 2048), (2, 33, 65), (16, 16, 64), (17, 100, 128), (64, 64, 192),
+    (65, 129, 1000), (127, 257, 511), (300, 1001, 1111), (512, 768, 384), (1030, 130, 260),
+])
+def test_linear_one_matrix(cuda_ok, M, N, K, dt):
+    check_linear([M], N, K, dt, seed=M + N, src=False)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("counts,N,K,div", [
+    ([0, 3, 0, 1, 16, 0, 17, 2], 96, 160, 4),        # decode-like
+    ([0] * 20 + [1] + [0] * 30, 64, 128, 1),         # a single row
+    ([5, 130, 0, 64, 300, 1], 200, 272, 6),
+    ([700, 0, 0, 20], 144, 129, 12),
+    ([257, 255, 256, 129], 520, 640, 3),
+    ([1] * 90, 70, 100, 2),
+    ([33, 40, 31, 65, 50, 0, 48, 90], 300, 2000, 5),
+])
+def test_linear_experts(cuda_ok, counts, N, K, div, dt):
+    check_linear(counts, N, K, dt, seed=N + K, div=div)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(scales=False), dict(pad=3), dict(wide=0), dict(wide=8), dict(wide=1), dict(src=False),
+    dict(extra=0), dict(extra=200),
+])
+def test_linear_variants(cuda_ok, kw):
+    for dt in (torch.float32, torch.bfloat16):
+        check_linear([40, 0, 150, 7], 136, 208, dt, div=1, **kw)
+
+
+def test_linear_no_rows_at_all(cuda_ok):
+    check_linear([0, 0, 0], 64, 128, torch.bfloat16, extra=9)
+    out = torch.full((0, 64), 1.0, device=DEV)
+    a = torch.zeros(1, 128, dtype=torch.int8, device=DEV)
+    B.moe_i8_linear(a, torch.ones(1, device=DEV), torch.zeros(1, 64, 128, dtype=torch.int8, device=DEV),
+                    None, out, row_src=torch.zeros(0, dtype=torch.int32, device=DEV))
+
+
+def test_linear_without_offsets_takes_every_row(cuda_ok):
+    for M in (1, 40, 333):
+        check_linear([M], 160, 224, torch.bfloat16, src=False, no_offsets=True)
+
+
+def test_linear_largest_sums_and_lowest_weights(cuda_ok):
+    """-128 weights against +-127 rows over K = 65536: sums near 2^30, exact."""
+    K, N, M = 65536, 8, 20
+    a = torch.full((M, K), 127, dtype=torch.int8)
+    a[1::2] = -127
+    w = torch.full((1, N, K), -128, dtype=torch.int8)
+    w[0, 3] = 127
+    out = torch.empty(M, N, device=DEV)
+    B.moe_i8_linear(a.to(DEV), torch.ones(M, device=DEV), w.to(DEV), None, out)
+    ref = a.double() @ w[0].double().t()
+    assert torch.all((f64(out) - ref).abs() <= U * ref.abs())
+
+
+def test_linear_nan_scale_marks_its_row_only(cuda_ok):
+    off, a, w, a_s, w_s, rows = linear_case([30, 20], 50, 96, torch.bfloat16, 3, src=False)
+    a_s[13] = float("nan")
+    out = torch.empty(50, 50, device=DEV)
+    B.moe_i8_linear(a.to(DEV), a_s.to(DEV), w.contiguous().to(DEV), w_s.to(DEV), out, offsets=off.to(DEV))
+    nan = torch.isnan(out).cpu()
+    assert nan[13].all() and int(nan.sum()) == 50
+
+
+@pytest.mark.parametrize("short", [True, False])
+def test_linear_matrices_past_32_bits(cuda_ok, short):
+    """540 matrices of 4 MiB: byte offsets past 2^31; the rows of the last
+    experts come from there."""
+    E, N, K = 540, 2048, 2048
+    counts = [0] * E
+    counts[0], counts[-1], counts[E - 3] = (3, 5, 2) if short else (200, 300, 1500)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32)
+    S = sum(counts)
+    w = torch.zeros(E, N, K, dtype=torch.int8, device=DEV)
+    for e in (0, E - 3, E - 1):
+        w[e] = torch.randint(-128, 128, (N, K), generator=gen(e)).to(torch.int8).to(DEV)
+    a = torch.randint(-127, 128, (S, K), generator=gen(1)).to(torch.int8)
+    a_s = torch.rand(S, generator=gen(2))
+    out = torch.empty(S, N, device=DEV)
+    B.moe_i8_linear(a.to(DEV), a_s.to(DEV), w, None, out, offsets=off.to(DEV))
+    for e in (0, E - 3, E - 1):
+        i, j = int(off[e]), int(off[e + 1])
+        ref = (a[i:j].to(DEV).double() @ w[e].double().t()) * a_s[i:j].to(DEV).double()[:, None]
+        assert torch.all((out[i:j].double() - ref).abs() <= ref.abs() * 3.1 * U)
+
+
+def test_row_sources_out_of_range_are_clamped(cuda_ok):
+    a = torch.randint(-127, 128, (4, 128), generator=gen(0)).to(torch.int8)
+    w = torch.randint(-128, 128, (1, 40, 128), generator=gen(1)).to(torch.int8)
+    src = torch.tensor([-9, 0, 7, 8, 1 << 30], dtype=torch.int32)
+    out = torch.empty(5, 40, device=DEV)
+    B.moe_i8_linear(a.to(DEV), torch.ones(4, device=DEV), w.to(DEV), None, out,
+                    row_src=src.to(DEV), row_div=2)
+    ref = (a.double() @ w[0].double().t())[torch.tensor([0, 0, 3, 3, 3])]
+    assert torch.equal(f64(out), ref)
+
+
+def test_offsets_behind_the_rows_are_clamped(cuda_ok):
+    """Offsets that say more rows than there are reach no row behind M."""
+    off, a, w, a_s, w_s, rows = linear_case([6, 10], 40, 96, torch.float32, 3, src=False)
+    big = off.clone()
+    big[2] = 4000
+    out = torch.full((20, 40), -77.0, device=DEV)
+    B.moe_i8_linear(a.to(DEV), a_s.to(DEV), w.contiguous().to(DEV), w_s.to(DEV), out[:16], offsets=big.to(DEV))
+    ref = linear_ref(off, a, w, a_s, w_s, None, 1)
+    assert torch.all((f64(out)[:16] - ref).abs() <= ref.abs() * 4.1 * U) and torch.all(out[16:] == -77)
+
+
+# ---------------------------------------------------------------- together --
+
+def experts_case(T, E, k, d, f, seed=0):
+    from sparse_moe_expert_fp32_amd.layer import DeviceLayer, Int8Experts
+    cfg = configs.LayerConfig("i8", 600 + T, T=T, d=d, E=E, k=k, f=128, r=4, group=32, act="bf16",
+                              router_bias_var=0.5)
+    L = DeviceLayer(cfg, inputs.generate(cfg, seed), device=DEV)
+    g = gen(seed)
+    gu = torch.randint(-127, 128, (E, 2 * f, d), generator=g).to(torch.int8)
+    dn = torch.randint(-127, 128, (E, d, f), generator=g).to(torch.int8)
+    s_gu = (torch.rand(E, 2 * f, generator=g) + 0.5) / (73 * d ** 0.5)
+    s_dn = (torch.rand(E, d, generator=g) + 0.5) / (73 * f ** 0.5)
+    X = Int8Experts(gu.to(DEV), s_gu.to(DEV), dn.to(DEV), s_dn.to(DEV))
+    return cfg, L, X
+
+
+@pytest.mark.parametrize("T,E,k,d,f", [(1, 40, 4, 256, 96), (64, 24, 3, 384, 112), (700, 6, 2, 256, 80)])
+def test_int8_experts_forward(cuda_ok, T, E, k, d, f):
+    """route -> permute -> int8 experts -> combine, stage by stage: each stage
+    against the definition on the GPU's own inputs to it."""
+    cfg, L, X = experts_case(T, E, k, d, f)
+    L.route()
+    L.permute()
+    gu = X.forward(L)
+    L.combine()
+    torch.cuda.synchronize()
+    x = L.t["x"].float().cpu()
+    q, s = quant_ref(x)
+    tok = L.perm_src.cpu().long() // k
+    off = L.offsets.cpu().tolist()
+    o = torch.zeros(cfg.S, d, dtype=torch.float64)
+    for e in range(E):
+        i, j = off[e], off[e + 1]
+        if j == i:
+            continue
+        # (the sums first, exact: a sum of 0 then stays 0)
+        ref = q[tok[i:j]].double() @ X.gate_up[e].cpu().double().t()
+        ref = ref * s[tok[i:j]].double()[:, None] * f64(X.s_gate_up[e])
+        assert torch.all((f64(gu[i:j]) - ref).abs() <= ref.abs() * (HALF[torch.bfloat16] + 5 * U))
+        g, u = f64(gu[i:j])[:, :f], f64(gu[i:j])[:, f:]
+        h = g * torch.sigmoid(g) * u
+        hs = h.abs().max(1).values / 127
+        wd = X.down[e].cpu().double() * f64(X.s_down[e])[:, None]
+        hq = torch.round(h / hs.clamp_min(1e-300)[:, None])
+        o[i:j] = (hq @ X.down[e].cpu().double().t()) * hs[:, None] * f64(X.s_down[e])
+        # a value next to a border may fall on either side: at most one step each
+        near = ((h / hs.clamp_min(1e-300)[:, None]).frac().abs() - 0.5).abs() < 1e-3
+        slack = near.double() * hs[:, None] @ wd.abs().t()
+        assert torch.all((f64(L.e_out[i:j]) - o[i:j]).abs() <=
+                         o[i:j].abs() * (HALF[torch.bfloat16] + 20 * U) + slack +
+                         20 * U * (h.abs() @ wd.abs().t()))
+    pos = L.slot_pos.cpu().long()
+    y = (f64(L.gates)[:, :, None] * f64(L.e_out)[pos].reshape(T, k, d)).sum(1)
+    assert torch.all((f64(L.y) - y).abs() <= y.abs() * HALF[torch.bfloat16] + 1e-5 * y.abs().max())
+
+
+@pytest.mark.parametrize("which", ["gate_up", "down"])
+def test_row_gradient(cuda_ok, which):
+    """The gradient of a product's rows by the same int8 product on the
+    transposed matrices: against the exact gradient of <dout, out>, off by at
+    most half a quantization step of every gradient value."""
+    cfg, L, X = experts_case(120, 5, 2, 256, 80)
+    L.route()
+    L.permute()
+    w, cs = (X.gate_up, X.s_gate_up) if which == "gate_up" else (X.down, X.s_down)
+    dout = torch.randn(cfg.S, w.shape[1], generator=gen(5)).bfloat16().to(DEV)
+    dx = X.rows_grad(which, dout, L.offsets)
+    torch.cuda.synchronize()
+    off = L.offsets.cpu().tolist()
+    for e in range(5):
+        i, j = off[e], off[e + 1]
+        if j == i:
+            continue
+        W = w[e].cpu().double()
+        v = f64(dout[i:j]) * f64(cs[e])
+        ref = v @ W                                  # d <dout, out> / d rows
+        step = v.abs().max(1).values / 127
+        tol = 0.5 * step[:, None] * W.abs().sum(0) * (1 + 1e-5) + HALF[torch.bfloat16] * ref.abs()
+        assert torch.all((f64(dx[i:j]) - ref).abs() <= tol * (1 + HALF[torch.bfloat16]) + 1e-30)
+        # and exactly the quantized definition
+        q, s = quant_ref(dout[i:j].float().cpu() * cs[e].cpu())
+        d = (q.double() @ W) * s.double()[:, None]
+        assert torch.all((f64(dx[i:j]) - d).abs() <= d.abs() * (HALF[torch.bfloat16] + 4 * U))
+
+
+def test_row_gradient_against_differences(cuda_ok):
+    """<dout, out(rows)> of the dequantized product is linear in the rows:
+    its difference along a direction is the gradient's product with it, up to
+    half a step of every quantized gradient value."""
+    N, K, M = 96, 64, 20
+    g = gen(2)
+    w = torch.randint(-127, 128, (1, N, K), generator=g).to(torch.int8).to(DEV)
+    cs = (torch.rand(1, N, generator=g) + 0.5).to(DEV) / 500
+    dout = torch.randn(M, N, generator=g).to(DEV)
+    from sparse_moe_expert_fp32_amd.layer import Int8Experts
+    X = Int8Experts(w, cs, w.transpose(1, 2).contiguous(), None)
+    dx = X.rows_grad("gate_up", dout, None)
+    W = f64(w[0]) * f64(cs[0])[:, None]
+    f = lambda r: (f64(dout) * (r @ W.t())).sum(1)  # noqa: E731
+    r0, step = torch.randn(M, K, generator=g).double(), torch.randn(M, K, generator=g).double()
+    diff = (f(r0 + step) - f(r0 - step)) / 2
+    v = f64(dout) * f64(cs[0])
+    slack = 0.5 * (v.abs().max(1).values / 127) * (step.abs() @ f64(w[0]).abs().t()).sum(1) * 1.001
+    assert torch.all((diff - (f64(dx) * step).sum(1)).abs() <= slack + 1e-6)
+
+
+def test_int8_experts_on_a_stream_and_in_a_graph(cuda_ok):
+    """Captured once, replayed between eager calls: the eager bits each time."""
+    cfg, L, X = experts_case(90, 12, 3, 256, 96)
+
+    def step():
+        L.route()
+        L.permute()
+        X.forward(L)
+        L.combine()
+
+    step()
+    torch.cuda.synchronize()
+    ref = L.y.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    assert torch.equal(L.y, ref)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(4):
+        L.y.fill_(0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(L.y, ref)
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(L.y, ref)
+
+
+def test_binding_refuses_wrong_tensors(cuda_ok):
+    z = lambda *n, dt=torch.int8: torch.zeros(*n, dtype=dt, device=DEV)  # noqa: E731
+    f = torch.float32
+    with pytest.raises(B.MoeError, match="adjacent"):
+        B.moe_quant_i8(z(64, 4, dt=f).t(), z(4, 128), z(4, dt=f))
+    with pytest.raises(B.MoeError, match="q must"):
+        B.moe_quant_i8(z(4, 200, dt=f), z(4, 128), z(4, dt=f))
+    with pytest.raises(B.MoeError, match="mul"):
+        B.moe_quant_i8(z(4, 100, dt=f), z(4, 128), z(4, dt=f), mul=z(4, 99, dt=f))
+    with pytest.raises(B.MoeError, match="w must"):
+        B.moe_i8_linear(z(4, 128), z(4, dt=f), z(1, 40, 128, dt=f), None, z(4, 40, dt=f))
+    with pytest.raises(B.MoeError, match="reach its stride"):
+        B.moe_i8_linear(z(4, 128), z(4, dt=f), z(1, 40 * 112)[:, :40 * 112 - 8].as_strided((1, 40, 100), (4480, 112, 1), 8),
+                        None, z(4, 40, dt=f))
+    with pytest.raises(B.MoeError, match="w_scale"):
+        B.moe_i8_linear(z(4, 128), z(4, dt=f), z(1, 40, 112), z(41, dt=f), z(4, 40, dt=f))
+    with pytest.raises(B.MoeError, match="multiple of 16"):
+        B.moe_i8_linear(z(4, 128), z(4, dt=f), z(1, 40, 100), None, z(4, 40, dt=f))

@@ -1,0 +1,419 @@
+"""Load-balance loss, gate gradient and router backward on the GPU against the
+formulas in float64, at the sizes and masks where they can go wrong.
+
+Tolerances count float32 roundings (U = 2^-24): n additions in any order carry
+at most n U of the sum of magnitudes; expf and the argument's rounding carry
+(|x| + 4) U of the exponential."""
+import numpy as np
+import pytest
+import torch
+
+from sparse_moe_expert_fp32_amd import binding as B, configs, inputs
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DEV = "cuda:0"
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def dims(T, d, E, k, act="bf16"):
+    return B.dims(T, d, E, k, 32, 1, 32, act)
+
+
+def f64(t):
+    return t.double().cpu()
+
+
+def route(T, E, k, seed, spread=1.0):
+    g = gen(seed)
+    l = torch.randn(T, E, generator=g) * spread
+    top = torch.topk(l, k, 1)
+    return l, top.indices.to(torch.int32), torch.softmax(top.values, 1)
+
+
+# ------------------------------------------------------------------ balance --
+
+def balance_ref(l, idx, valid, dloss):
+    T, E = l.shape
+    k = idx.shape[1]
+    on = torch.ones(T, dtype=torch.bool) if valid is None else valid
+    n = int(on.sum())
+    counts = torch.zeros(E + 1, dtype=torch.int64)
+    p = torch.zeros(T, E, dtype=torch.float64)
+    for t in range(T):
+        if on[t]:
+            row = l[t].double()
+            m = row.max()
+            if m > -np.inf:
+                z = torch.exp(row - m)
+                p[t] = z / z.sum()
+            for e in idx[t].tolist():
+                if 0 <= e < E:
+                    counts[e] += 1
+    counts[E] = n
+    if n == 0:
+        return 0.0, counts, torch.zeros(E, dtype=torch.float64), torch.zeros(T, E, dtype=torch.float64), p
+    prob = p.sum(0) / n
+    loss = E * float((counts[:E] / (n * k) * prob).sum())
+    w = dloss * E * counts[:E].double() / (n * n * k)
+    return loss, counts, prob, p * (w - (p * w).sum(1, keepdim=True)), p
+
+
+def balance_gpu(l, idx, valid, dloss, in_place=False):
+    T, E = l.shape
+    dm = dims(T, 32, E, idx.shape[1])
+    new = lambda *n, dt=torch.float32: torch.full(n, -77, dtype=dt, device=DEV)  # noqa: E731
+    loss, counts, prob, stats = new(1), new(E + 1, dt=torch.int32), new(E), new(T, 2)
+    ws = new(max(1, B.moe_workspace_size(dm, B.CALL_BALANCE_FWD)), dt=torch.int8)
+    ld, idxd = l.to(DEV), idx.to(DEV)
+    v = None if valid is None else valid.to(DEV)
+    dl = torch.tensor([dloss], device=DEV)
+    out = ld if in_place else new(T, E)
+    B.moe_balance_fwd(dm, ld, idxd, v, loss, counts, prob, stats, ws)
+    B.moe_balance_bwd(dm, ld, stats, counts, v, dl, out)
+    torch.cuda.synchronize()
+    return loss, counts, prob, stats, out
+
+
+def check_balance(l, idx, valid, dloss=0.5, in_place=False):
+    loss, counts, prob, stats, out = balance_gpu(l, idx, valid, dloss, in_place)
+    rl, rc, rp, rd, p = balance_ref(l, idx, valid, dloss)
+    T, E = l.shape
+    n, k = int(rc[E]), idx.shape[1]
+    assert torch.equal(counts.cpu().long(), rc)
+    fin = torch.where(torch.isfinite(l), l, torch.zeros_like(l)).double()
+    span = float((fin.max() - fin.min())) if n else 0.0
+    rel_p = (span + 4 + E // 64 + 8 + 4) * U           # exp, the row's sum, two multiplications
+    rel = rel_p + (T + 8) * U                          # the sum over tokens, all terms >= 0
+    assert torch.all((f64(prob) - rp).abs() <= rel * rp + 1e-38)
+    assert abs(float(loss) - rl) <= (rel + 4 * U) * rl + 1e-38
+    wmax = abs(dloss) * E * float(rc[:E].max()) / max(1, n * n * k)
+    assert torch.all((f64(out) - rd).abs() <= (3 * rel_p + (E // 64 + 12) * U) * p * wmax * 2 + 1e-38)
+    if valid is not None:
+        assert torch.all(out.cpu()[~valid] == 0) and torch.all(stats.cpu()[~valid] == 0)
+
+
+@pytest.mark.parametrize("T,E,k", [
+    (1, 1, 1), (1, 8, 2), (3, 64, 6), (64, 8, 2), (77, 65, 5), (130, 256, 32), (61, 257, 1),
+    (200, 460, 12), (33, 513, 8), (19, 1024, 32), (2600, 12, 3),
+])
+def test_balance(cuda_ok, T, E, k):
+    l, idx, _ = route(T, E, k, T + E)
+    check_balance(l, idx, None)
+
+
+@pytest.mark.parametrize("T,E,k", [(5, 8, 2), (301, 100, 4), (65, 460, 12)])
+def test_balance_masked_tokens_hold_anything(cuda_ok, T, E, k):
+    l, idx, _ = route(T, E, k, 3 * T)
+    valid = torch.rand(T, generator=gen(T)) > 0.4
+    valid[0], valid[-1] = False, True
+    l[~valid] = float("nan")
+    idx[~valid] = 1 << 30
+    check_balance(l, idx, valid)
+    check_balance(l, idx, valid, in_place=True)
+
+
+def test_balance_without_a_token(cuda_ok):
+    l, idx, _ = route(9, 20, 3, 1)
+    check_balance(l * float("inf"), idx, torch.zeros(9, dtype=torch.bool))
+
+
+def test_balance_masked_experts_and_empty_rows(cuda_ok):
+    """-inf logits have probability 0, a row of them adds nothing; the type's
+    lowest value is a finite logit like others; same index twice, and indices
+    out of range."""
+    l, idx, _ = route(70, 90, 4, 2)
+    l[:, 7] = -np.inf
+    l[3] = -np.inf
+    l[4, 5:] = -np.inf
+    l[5] = torch.finfo(torch.float32).min
+    l[6, 10] = torch.finfo(torch.float32).min
+    idx[8] = 2
+    idx[9, 1], idx[9, 2] = -1, 90
+    T, E = l.shape
+    loss, counts, prob, stats, out = balance_gpu(l, idx, None, 1.0)
+    rl, rc, rp, rd, p = balance_ref(l, idx, None, 1.0)
+    assert torch.equal(counts.cpu().long(), rc) and counts[2] >= 4
+    rel = (16 + 4 + 2 + 12 + T + 8) * U
+    assert torch.all((f64(prob) - rp).abs() <= rel * rp)
+    assert abs(float(loss) - rl) <= rel * rl
+    others = [t for t in range(T) if t != 5]        # (row 5 is even over all experts)
+    assert torch.all(out[3] == 0) and torch.all(out[others, 7] == 0)
+    assert torch.all((f64(out) - rd).abs() <= 8 * rel * p * float(rc[:E].max()) * E / (T * T * 4))
+
+
+def test_balance_nan_is_not_hidden(cuda_ok):
+    l, idx, _ = route(40, 70, 4, 5)
+    l[13, 50] = float("nan")
+    loss, counts, prob, stats, out = balance_gpu(l, idx, None, 1.0)
+    assert torch.isnan(loss).all() and torch.isnan(prob).all()
+    assert torch.isnan(out[13]).all() and torch.isfinite(out[14]).all()
+    assert counts[70] == 40
+
+
+def test_balance_gradient_against_differences(cuda_ok):
+    """Central differences of the float64 loss with the counts held fixed."""
+    l, idx, _ = route(6, 9, 2, 8)
+    *_, out = balance_gpu(l, idx, None, 1.0)
+    counts = balance_ref(l, idx, None, 1.0)[1][:9].double()
+    def loss(x):
+        return 9 * float((counts / 12 * torch.softmax(x, 1).mean(0)).sum())
+    h = 1e-5
+    for t, e in ((0, 0), (2, 5), (5, 8), (3, 3)):
+        a, b = l.double().clone(), l.double().clone()
+        a[t, e] += h
+        b[t, e] -= h
+        # (the differences' own error: h^2 of the third derivative, and 2^-52 / h)
+        assert abs((loss(a) - loss(b)) / (2 * h) - float(out[t, e])) <= 1e-9 + 60 * U
+
+
+# --------------------------------------------------------------------- gate --
+
+def act_t(act):
+    return torch.bfloat16 if act == "bf16" else torch.float32
+
+
+def gate_case(T, d, E, k, act, seed):
+    g = gen(seed)
+    l, idx, gates = route(T, E, k, seed)
+    dy = torch.randn(T, d, generator=g).to(act_t(act))
+    e_out = torch.randn(T * k, d, generator=g).to(act_t(act))
+    pos = torch.randperm(T * k, generator=g).to(torch.int32).reshape(T, k)
+    dl = torch.randn(T, E, generator=g)
+    return dy, e_out, idx, gates, pos, dl
+
+
+def gate_ref(dy, e_out, idx, gates, pos, valid, dl):
+    T, k = idx.shape
+    o = e_out.double()[pos.long()]
+    prod = dy.double()[:, None, :] * o
+    dg, mag = prod.sum(2), prod.abs().sum(2)
+    g = gates.double()
+    dsel = g * (dg - (g * dg).sum(1, keepdim=True))
+    size = g * (mag + (g * mag).sum(1, keepdim=True))
+    tot = torch.zeros(T, dl.shape[1] if dl is not None else 0, dtype=torch.float64)
+    return dsel, size
+
+
+def check_gate(T, d, E, k, act, valid=None, dl_given=True, in_place=False, dup=False):
+    dy, e_out, idx, gates, pos, dl = gate_case(T, d, E, k, act, T + 7 * k)
+    if dup:
+        idx[:, 1] = idx[:, 0]
+    if valid is not None:
+        dy[~valid] = float("nan")
+    dm = dims(T, d, E, k, act)
+    dd = [t.to(DEV) for t in (dy, e_out, idx, gates, pos)]
+    v = None if valid is None else valid.to(DEV)
+    src = dl.to(DEV) if dl_given else None
+    out = src if in_place else torch.full((T, E), -77.0, device=DEV)
+    B.moe_gate_bwd(dm, *dd, v, src, out)
+    torch.cuda.synchronize()
+    dsel, size = gate_ref(dy, e_out, idx, gates, pos, valid, dl)
+    ref = dl.double().clone() if dl_given else torch.zeros(T, E, dtype=torch.float64)
+    tol = ref.abs() * 4 * U
+    tol.scatter_add_(1, idx.long(), (d / 64 + 3 * k + 24) * U * size)
+    ref.scatter_add_(1, idx.long(), dsel)
+    on = torch.ones(T, dtype=torch.bool) if valid is None else valid
+    assert torch.all((f64(out) - ref).abs()[on] <= tol[on] + 1e-38)
+    assert torch.all(out.cpu()[~on] == 0)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d,E,k", [
+    (1, 32, 1, 1), (1, 128, 8, 2), (5, 2048, 460, 12), (63, 96, 65, 3), (33, 1056, 20, 5),
+    (18, 544, 40, 8), (9, 320, 1024, 32), (130, 64, 64, 6), (7, 256, 48, 13),
+])
+def test_gate_bwd(cuda_ok, T, d, E, k, act):
+    check_gate(T, d, E, k, act)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dl_given=False), dict(in_place=True), dict(dup=True), dict(dup=True, in_place=True),
+    dict(valid=True), dict(valid=True, in_place=True), dict(valid=True, dl_given=False),
+])
+def test_gate_bwd_variants(cuda_ok, kw):
+    kw = dict(kw)
+    if kw.get("valid"):
+        kw["valid"] = torch.arange(50) % 3 != 0
+    check_gate(50, 160, 70, 6, "bf16", **kw)
+
+
+# ------------------------------------------------------------------- router --
+
+def router_case(T, d, E, act, seed):
+    g = gen(seed)
+    x = torch.randn(T, d, generator=g).to(act_t(act))
+    w = torch.randn(d, E, generator=g) / d ** 0.5
+    dl = torch.randn(T, E, generator=g) * torch.rand(T, 1, generator=g)
+    dx_in = torch.randn(T, d, generator=g).to(act_t(act))
+    return x, w, dl, dx_in
+
+
+def run_router(dm, x, w, valid, dl, dx_in, want, alias=False):
+    T, d, E, dt = dm.T, dm.d_model, dm.n_experts, x.dtype
+    to = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    xin = to(dx_in) if "x" in want else None
+    dx = (xin if alias else torch.full((T, d), -77.0, device=DEV, dtype=dt)) if "x" in want else None
+    dw = torch.full((d, E), -77.0, device=DEV) if "w" in want else None
+    db = torch.full((E,), -77.0, device=DEV) if "b" in want else None
+    ws = torch.full((max(1, B.moe_workspace_size(dm, B.CALL_ROUTER_BWD)),), 255, dtype=torch.uint8, device=DEV)
+    B.moe_router_bwd(dm, to(x), to(w), to(valid), to(dl), xin, dx, dw, db, ws)
+    torch.cuda.synchronize()
+    return dx, dw, db
+
+
+def check_router(T, d, E, act, want="xwb", valid=None, dx_given=True, alias=False):
+    x, w, dl, dx_in = router_case(T, d, E, act, T + d + E)
+    on = torch.ones(T, dtype=torch.bool) if valid is None else valid
+    xd, dld = x.double(), dl.double()
+    xd[~on], dld[~on] = 0, 0
+    if valid is not None:
+        x[~on], dl[~on] = float("nan"), float("inf")
+    dx, dw, db = run_router(dims(T, d, E, 1, act), x, w, valid, dl, dx_in if dx_given else None, want, alias)
+    if dx is not None:
+        ref = dld @ w.double().t() + (dx_in.double() if dx_given else 0.0)
+        mag = dld.abs() @ w.double().abs().t()
+        half = 2.0 ** -8 if act == "bf16" else 2.0 ** -24
+        # float32: E + 4 additions; bf16 output: each operand kept to 16 bits
+        # or more (2^-17 each, and the product of two remainders 2^-16)
+        tol = half * ref.abs() * (1 + half) + (E + 8) * U * (mag + ref.abs()) + (2.0 ** -15 * mag if act == "bf16" else 0)
+        assert torch.all((f64(dx) - ref).abs() <= tol + 1e-38)
+    n = int(on.sum())
+    if dw is not None:
+        ref, mag = xd.t() @ dld, xd.abs().t() @ dld.abs()
+        assert torch.all((f64(dw) - ref).abs() <= (n + 12) * U * mag + 1e-38)
+        if n > 1000:   # far from the worst case: additions of random sign
+            assert float((f64(dw) - ref).norm() / ref.norm()) <= 2e-6
+    if db is not None:
+        assert torch.all((f64(db) - dld.sum(0)).abs() <= (n + 12) * U * dld.abs().sum(0) + 1e-38)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d,E", [
+    (1, 32, 1), (1, 128, 8), (64, 128, 8), (3, 2048, 460), (130, 96, 65), (257, 416, 33),
+    (100, 1120, 1024), (511, 160, 127), (1500, 256, 130),
+])
+def test_router_bwd(cuda_ok, T, d, E, act):
+    check_router(T, d, E, act)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("kw", [
+    dict(want="x"), dict(want="w"), dict(want="b"), dict(want="xb"), dict(want="wb"),
+    dict(dx_given=False), dict(alias=True), dict(valid=True), dict(valid=True, alias=True),
+    dict(valid=True, dx_given=False, want="x"), dict(valid="none"),
+])
+def test_router_bwd_variants(cuda_ok, act, kw):
+    kw = dict(kw)
+    if kw.get("valid") == "none":
+        kw["valid"] = torch.zeros(150, dtype=torch.bool)
+    elif kw.get("valid"):
+        kw["valid"] = torch.rand(150, generator=gen(4)) > 0.3
+    check_router(150, 224, 70, act, **kw)
+
+
+def test_router_bwd_is_repeatable(cuda_ok):
+    x, w, dl, dx_in = router_case(2000, 256, 100, "bf16", 9)
+    a = run_router(dims(2000, 256, 100, 1), x, w, None, dl, dx_in, "xwb")
+    b = run_router(dims(2000, 256, 100, 1), x, w, None, dl, dx_in, "xwb")
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+# ----------------------------------------------------------------- together --
+
+def layer(T=300, E=24, k=4, act="bf16", seed=0, d=256):
+    from sparse_moe_expert_fp32_amd.layer import DeviceLayer
+    cfg = configs.LayerConfig("rt", 500, T=T, d=d, E=E, k=k, f=128, r=16,
+                              group=128, act=act, router_bias_var=0.5, train=True)
+    L = DeviceLayer(cfg, inputs.generate(cfg, seed), device=DEV, want_logits=True)
+    L.init_router_training()
+    L.bal_dloss.fill_(0.3)
+    return cfg, L
+
+
+RESULTS = ("bal_loss", "bal_counts", "bal_prob", "dlogits", "dx", "dw_router", "db_router")
+
+
+def test_layer_router_training_step(cuda_ok):
+    """A float32 layer: the router's gradients of loss = <dy, y> + 0.3 balance
+    against float64 autograd through router, softmax gates and the experts'
+    outputs, with the selection held fixed."""
+    cfg, L = layer(T=60, E=12, k=3, act="f32", d=128)
+    L.router_train_step()
+    torch.cuda.synchronize()
+    x, w, b = (f64(L.t[n]) for n in ("x", "w_router", "b_router"))
+    w.requires_grad_(True)
+    b.requires_grad_(True)
+    logits = x @ w + b
+    idx = L.topk_idx.cpu().long()
+    gates = torch.softmax(logits.gather(1, idx), 1)
+    o = f64(L.e_out)[L.slot_pos.cpu().long()].reshape(cfg.T, cfg.k, cfg.d)
+    y = (gates[:, :, None] * o).sum(1)
+    counts = torch.bincount(idx.reshape(-1), minlength=cfg.E).double()
+    bal = cfg.E * (counts / cfg.S * torch.softmax(logits, 1).mean(0)).sum()
+    ((y * f64(L.t["dy"])).sum() + 0.3 * bal).backward()
+    assert abs(float(L.bal_loss) - float(bal.detach())) <= 1e-5 * float(bal.detach())
+    # float32 logits over d = 128 and dot products over d: 1e-5 of the norm
+    for got, ref in ((L.dw_router, w.grad), (L.db_router, b.grad)):
+        assert float((f64(got) - ref).norm() / ref.norm()) <= 1e-5
+
+
+def test_router_training_dx_adds_the_balance_share(cuda_ok):
+    cfg, L = layer()
+    L.train_step()
+    torch.cuda.synchronize()
+    before = f64(L.dx)
+    L.balance()
+    L.router_bwd()
+    torch.cuda.synchronize()
+    share = f64(L.dlogits_bal) @ f64(L.t["w_router"]).t()
+    ref = before + share
+    assert torch.all((f64(L.dx) - ref).abs() <= 2.0 ** -8 * ref.abs() * 1.01 + 1e-6 * share.abs().max())
+
+
+def test_router_training_on_a_side_stream_and_in_a_graph(cuda_ok):
+    """The step captured once and replayed between eager steps of the same
+    layer gives the eager bits on every replay."""
+    cfg, L = layer()
+    valid = (torch.arange(cfg.T) % 5 != 0).to(DEV)
+    L.router_train_step(valid)
+    torch.cuda.synchronize()
+    ref = {n: getattr(L, n).clone() for n in RESULTS}
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        L.router_train_step(valid)
+    torch.cuda.synchronize()
+    assert all(torch.equal(getattr(L, n), ref[n]) for n in RESULTS)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        L.router_train_step(valid)
+    for _ in range(4):
+        for n in RESULTS:
+            getattr(L, n).fill_(-3)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(getattr(L, n), ref[n]) for n in RESULTS)
+        L.router_train_step(valid)
+        torch.cuda.synchronize()
+        assert all(torch.equal(getattr(L, n), ref[n]) for n in RESULTS)
+
+
+def test_binding_refuses_wrong_tensors(cuda_ok):
+    cfg, L = layer(T=20, E=8, k=2)
+    L.forward()
+    with pytest.raises(B.MoeError, match="counts"):
+        B.moe_balance_fwd(L.dm, L.logits, L.topk_idx, None, L.bal_loss, L.bal_counts[:-1],
+                          L.bal_prob, L.bal_stats, L.ws[B.CALL_BALANCE_FWD])
+    with pytest.raises(B.MoeError, match="logits"):
+        B.moe_balance_bwd(L.dm, L.logits.t(), L.bal_stats, L.bal_counts, None, L.bal_dloss, L.dlogits)
+    with pytest.raises(B.MoeError, match="dx "):
+        B.moe_router_bwd(L.dm, L.t["x"], L.t["w_router"], None, L.dlogits, None, L.dx.float(),
+                         None, None, L.ws[B.CALL_ROUTER_BWD])
+    with pytest.raises(B.MoeError, match="valid"):
+        B.moe_gate_bwd(L.dm, L.t["dy"], L.e_out, L.topk_idx, L.gates, L.slot_pos,
+                       torch.ones(19, dtype=torch.bool, device=DEV), None, L.dlogits)

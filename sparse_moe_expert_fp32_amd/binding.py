@@ -278,37 +278,52 @@ def moe_adamw_step(h: AdamWHparams, master, grad, m, v, param=None, stream=None)
 # types, sizes and layouts are checked here (the C ABI sees pointers only),
 # and the call runs with the tensors' device current.
 
-_F32, _I32, _I8 = torch.float32, torch.int32, torch.int8
+_F32, _I32, _I8, _U8, _BF16 = (torch.float32, torch.int32, torch.int8, torch.uint8,
+                               torch.bfloat16)
 _ACT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_DT = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
 
 
-def _need(ok, name, what):
-    if not ok:
-        raise MoeError(f"{name}: {what}")
+def _gpu(name, t) -> int:
+    """Index of the GPU that t is on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise MoeError(f"{name}: tensors must be on the GPU, got {t.device}")
+    return dev
 
 
-def _dense(name, arg, t, dtypes, numel, dev):
-    """One contiguous device tensor of `numel` elements of one of `dtypes`."""
-    if t.dtype not in dtypes or t.numel() != numel or t.device != dev or not t.is_contiguous():
-        raise MoeError(f"{name}: {arg} must be a contiguous {'/'.join(str(d) for d in dtypes)} "
-                       f"tensor of {numel} elements on {dev}, got {t.dtype} {tuple(t.shape)} "
-                       f"on {t.device}")
+def _dense(name, arg, t, dtype, numel, dev):
+    """Pointer of a contiguous tensor of `numel` elements on GPU `dev`."""
+    if t.dtype is not dtype or t.numel() != numel or t.get_device() != dev or \
+            not t.is_contiguous():
+        raise MoeError(f"{name}: {arg} must be a contiguous {dtype} tensor of {numel} elements "
+                       f"on GPU {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _checked(name, dev, *specs):
-    if dev.type != "cuda":
-        raise MoeError(f"{name}: tensors must be on the GPU, got {dev}")
-    for arg, t, dtypes, numel in specs:
-        if t is not None:
-            _dense(name, arg, t, dtypes, numel, dev)
+def _opt(name, arg, t, dtype, numel, dev):
+    return None if t is None else _dense(name, arg, t, dtype, numel, dev)
+
+
+def _valid(name, t, T, dev):
+    if t is None:
+        return None
+    return _dense(name, "valid", t, _U8 if t.dtype is _U8 else torch.bool, T, dev)
+
+
+def _ws(name, ws, dev):
+    if ws is None:
+        return None, 0
+    n = ws.numel() * ws.element_size()
+    return _dense(name, "ws", ws, ws.dtype, ws.numel(), dev), n
 
 
 def _call(name, dev, fn, args, stream):
-    """Call fn(*args, stream) with `dev` current, on its current stream
-    unless one is given."""
-    if dev.index == torch.cuda.current_device():
-        st = _stream(stream)
-        status = fn(*args, st)
+    """fn(*args, stream) with GPU `dev` current, on its current stream unless
+    one is given."""
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                    else _stream(stream))
     else:
         with torch.cuda.device(dev):
             status = fn(*args, _stream(stream))
@@ -316,71 +331,56 @@ def _call(name, dev, fn, args, stream):
         _check(status, name)
 
 
-def _bytes(ws):
-    return 0 if ws is None else ws.numel() * ws.element_size()
-
-
-_BOOLS = (torch.bool, torch.uint8)
-
-
 def moe_balance_fwd(dm: Dims, logits, topk_idx, valid, loss, counts, prob, stats, ws, stream=None):
     """Load-balance loss, per-expert counts (and the number of tokens, last)
     and mean probabilities; `stats` is what moe_balance_bwd reads."""
-    T, E, dev = dm.T, dm.n_experts, logits.device
-    _checked("moe_balance_fwd", dev, ("logits", logits, (_F32,), T * E),
-             ("topk_idx", topk_idx, (_I32,), T * dm.top_k), ("valid", valid, _BOOLS, T),
-             ("loss", loss, (_F32,), 1), ("counts", counts, (_I32,), E + 1),
-             ("prob", prob, (_F32,), E), ("stats", stats, (_F32,), 2 * T))
-    _need(ws is None or ws.device == dev, "moe_balance_fwd", "ws is on another device")
-    _call("moe_balance_fwd", dev, LIB.moe_balance_fwd,
-          (ctypes.byref(dm), _p(logits), _p(topk_idx), _p(valid), _p(loss), _p(counts), _p(prob),
-           _p(stats), _p(ws), _bytes(ws)), stream)
+    f, T, E, dev = "moe_balance_fwd", dm.T, dm.n_experts, _gpu("moe_balance_fwd", logits)
+    _call(f, dev, LIB.moe_balance_fwd,
+          (dm, _dense(f, "logits", logits, _F32, T * E, dev),
+           _dense(f, "topk_idx", topk_idx, _I32, T * dm.top_k, dev), _valid(f, valid, T, dev),
+           _dense(f, "loss", loss, _F32, 1, dev), _dense(f, "counts", counts, _I32, E + 1, dev),
+           _dense(f, "prob", prob, _F32, E, dev), _dense(f, "stats", stats, _F32, 2 * T, dev),
+           *_ws(f, ws, dev)), stream)
 
 
 def moe_balance_bwd(dm: Dims, logits, stats, counts, valid, dloss, dlogits, stream=None):
     """Gradient of the load-balance loss with respect to the logits."""
-    T, E, dev = dm.T, dm.n_experts, logits.device
-    _checked("moe_balance_bwd", dev, ("logits", logits, (_F32,), T * E),
-             ("stats", stats, (_F32,), 2 * T), ("counts", counts, (_I32,), E + 1),
-             ("valid", valid, _BOOLS, T), ("dloss", dloss, (_F32,), 1),
-             ("dlogits", dlogits, (_F32,), T * E))
-    _call("moe_balance_bwd", dev, LIB.moe_balance_bwd,
-          (ctypes.byref(dm), _p(logits), _p(stats), _p(counts), _p(valid), _p(dloss),
-           _p(dlogits)), stream)
-
-
-def _act_of(dm):
-    return (torch.bfloat16,) if dm.act == MOE_BF16 else (torch.float32,)
+    f, T, E, dev = "moe_balance_bwd", dm.T, dm.n_experts, _gpu("moe_balance_bwd", logits)
+    _call(f, dev, LIB.moe_balance_bwd,
+          (dm, _dense(f, "logits", logits, _F32, T * E, dev),
+           _dense(f, "stats", stats, _F32, 2 * T, dev),
+           _dense(f, "counts", counts, _I32, E + 1, dev), _valid(f, valid, T, dev),
+           _dense(f, "dloss", dloss, _F32, 1, dev),
+           _dense(f, "dlogits", dlogits, _F32, T * E, dev)), stream)
 
 
 def moe_gate_bwd(dm: Dims, dy, e_out, topk_idx, gates, slot_pos, valid, dlogits_in, dlogits,
                  stream=None):
     """dlogits = dlogits_in + the gates' gradient with respect to the logits."""
-    T, E, k, d, dev = dm.T, dm.n_experts, dm.top_k, dm.d_model, dy.device
-    _checked("moe_gate_bwd", dev, ("dy", dy, _act_of(dm), T * d),
-             ("e_out", e_out, _act_of(dm), T * k * d), ("topk_idx", topk_idx, (_I32,), T * k),
-             ("gates", gates, (_F32,), T * k), ("slot_pos", slot_pos, (_I32,), T * k),
-             ("valid", valid, _BOOLS, T), ("dlogits_in", dlogits_in, (_F32,), T * E),
-             ("dlogits", dlogits, (_F32,), T * E))
-    _call("moe_gate_bwd", dev, LIB.moe_gate_bwd,
-          (ctypes.byref(dm), _p(dy), _p(e_out), _p(topk_idx), _p(gates), _p(slot_pos), _p(valid),
-           _p(dlogits_in), _p(dlogits)), stream)
+    f, T, E, k, d, act = "moe_gate_bwd", dm.T, dm.n_experts, dm.top_k, dm.d_model, _DT.get(dm.act)
+    dev = _gpu(f, dy)
+    _call(f, dev, LIB.moe_gate_bwd,
+          (dm, _dense(f, "dy", dy, act, T * d, dev),
+           _dense(f, "e_out", e_out, act, T * k * d, dev),
+           _dense(f, "topk_idx", topk_idx, _I32, T * k, dev),
+           _dense(f, "gates", gates, _F32, T * k, dev),
+           _dense(f, "slot_pos", slot_pos, _I32, T * k, dev), _valid(f, valid, T, dev),
+           _opt(f, "dlogits_in", dlogits_in, _F32, T * E, dev),
+           _dense(f, "dlogits", dlogits, _F32, T * E, dev)), stream)
 
 
 def moe_router_bwd(dm: Dims, x, w_router, valid, dlogits, dx_in, dx, dw_router, db_router, ws,
                    stream=None):
     """dx = dx_in + dlogits W_r^T, dw_router = x^T dlogits, db_router = the
     column sums of dlogits; each output may be None."""
-    T, E, d, dev = dm.T, dm.n_experts, dm.d_model, dlogits.device
-    _checked("moe_router_bwd", dev, ("x", x, _act_of(dm), T * d),
-             ("w_router", w_router, (_F32,), d * E), ("valid", valid, _BOOLS, T),
-             ("dlogits", dlogits, (_F32,), T * E), ("dx_in", dx_in, _act_of(dm), T * d),
-             ("dx", dx, _act_of(dm), T * d), ("dw_router", dw_router, (_F32,), d * E),
-             ("db_router", db_router, (_F32,), E))
-    _need(ws is None or ws.device == dev, "moe_router_bwd", "ws is on another device")
-    _call("moe_router_bwd", dev, LIB.moe_router_bwd,
-          (ctypes.byref(dm), _p(x), _p(w_router), _p(valid), _p(dlogits), _p(dx_in), _p(dx),
-           _p(dw_router), _p(db_router), _p(ws), _bytes(ws)), stream)
+    f, T, E, d, act = "moe_router_bwd", dm.T, dm.n_experts, dm.d_model, _DT.get(dm.act)
+    dev = _gpu(f, dlogits)
+    _call(f, dev, LIB.moe_router_bwd,
+          (dm, _opt(f, "x", x, act, T * d, dev), _opt(f, "w_router", w_router, _F32, d * E, dev),
+           _valid(f, valid, T, dev), _dense(f, "dlogits", dlogits, _F32, T * E, dev),
+           _opt(f, "dx_in", dx_in, act, T * d, dev), _opt(f, "dx", dx, act, T * d, dev),
+           _opt(f, "dw_router", dw_router, _F32, d * E, dev),
+           _opt(f, "db_router", db_router, _F32, E, dev), *_ws(f, ws, dev)), stream)
 
 
 def moe_i8_stride(K: int) -> int:
@@ -388,71 +388,71 @@ def moe_i8_stride(K: int) -> int:
     return (K + 127) // 128 * 128
 
 
-def _rows(name, arg, t, dtypes, dev):
+def _rows(name, arg, t, dtype, dev):
     """(rows, columns, row stride) of a matrix whose columns are adjacent."""
-    if t.dim() != 2 or t.dtype not in dtypes or t.device != dev or \
-            (t.stride(1) != 1 and t.shape[1] > 1):
-        raise MoeError(f"{name}: {arg} must be a {'/'.join(str(d) for d in dtypes)} matrix on "
-                       f"{dev} with adjacent columns, got {t.dtype} {tuple(t.shape)} "
-                       f"{t.stride()} on {t.device}")
-    M, N = t.shape
-    return M, N, t.stride(0) if M > 1 else max(t.stride(0), N)
+    if t.dim() == 2 and t.dtype is dtype and t.get_device() == dev:
+        M, N = t.shape
+        ld, one = t.stride()
+        if one == 1 or N <= 1:
+            return M, N, ld if ld > N or M > 1 else N
+    raise MoeError(f"{name}: {arg} must be a {dtype} matrix on GPU {dev} with adjacent columns, "
+                   f"got {t.dtype} {tuple(t.shape)} {t.stride()} on {t.device}")
 
 
-def _experts(name, offsets, E, dev):
-    if offsets is not None:
-        _dense(name, "offsets", offsets, (_I32,), E + 1, dev)
+def _act_code(name, arg, t) -> int:
+    a = _ACT.get(t.dtype)
+    if a is None:
+        raise MoeError(f"{name}: {arg} must be float32 or bfloat16, got {t.dtype}")
+    return a
 
 
 def moe_quant_i8(x, q, scale, mul=None, col_scale=None, offsets=None, stream=None):
     """Rows of x (or silu(x) mul, or x col_scale[expert]) -> int8 rows q
     [M][moe_i8_stride(K)] and their scales [M]."""
-    name, dev = "moe_quant_i8", x.device
-    _need(dev.type == "cuda", name, f"tensors must be on the GPU, got {dev}")
-    M, K, ldx = _rows(name, "x", x, tuple(_ACT), dev)
-    Mq, Kq, ldq = _rows(name, "q", q, (_I8,), dev)
-    _need(Mq == M and Kq >= moe_i8_stride(K), name,
-          f"q must have {M} rows of at least {moe_i8_stride(K)} values, got {tuple(q.shape)}")
-    _dense(name, "scale", scale, (_F32,), M, dev)
+    f, dev, act = "moe_quant_i8", _gpu("moe_quant_i8", x), _act_code("moe_quant_i8", "x", x)
+    M, K, ldx = _rows(f, "x", x, x.dtype, dev)
+    Mq, Kq, ldq = _rows(f, "q", q, _I8, dev)
+    if Mq != M or Kq < moe_i8_stride(K):
+        raise MoeError(f"{f}: q must have {M} rows of at least {moe_i8_stride(K)} values, "
+                       f"got {tuple(q.shape)}")
     ldm, E = 0, 1
     if mul is not None:
-        Mm, Km, ldm = _rows(name, "mul", mul, (x.dtype,), dev)
-        _need((Mm, Km) == (M, K), name, f"mul must be {(M, K)}, got {tuple(mul.shape)}")
+        Mm, Km, ldm = _rows(f, "mul", mul, x.dtype, dev)
+        if Mm != M or Km != K:
+            raise MoeError(f"{f}: mul must be {(M, K)}, got {tuple(mul.shape)}")
     if offsets is not None:
         E = offsets.numel() - 1
-        _experts(name, offsets, E, dev)
-    if col_scale is not None:
-        _dense(name, "col_scale", col_scale, (_F32,), E * K, dev)
-    _call(name, dev, LIB.moe_quant_i8,
-          (M, K, _ACT[x.dtype], _p(x), ldx, _p(mul), ldm, _p(col_scale), _p(offsets), E, _p(q),
-           ldq, _p(scale)), stream)
+    _call(f, dev, LIB.moe_quant_i8,
+          (M, K, act, x.data_ptr(), ldx, _p(mul), ldm,
+           _opt(f, "col_scale", col_scale, _F32, E * K, dev),
+           _opt(f, "offsets", offsets, _I32, E + 1, dev), E, q.data_ptr(), ldq,
+           _dense(f, "scale", scale, _F32, M, dev)), stream)
 
 
 def moe_i8_linear(a, a_scale, w, w_scale, out, offsets=None, row_src=None, row_div=1,
                   stream=None):
     """out[p] = rows a (int8, as moe_quant_i8 writes them) by the int8 matrix
     w[e] [N][K] of the row's expert, scaled per row and per channel."""
-    name, dev = "moe_i8_linear", a.device
-    _need(dev.type == "cuda", name, f"tensors must be on the GPU, got {dev}")
-    R, Ka, lda = _rows(name, "a", a, (_I8,), dev)
-    M, N, ldo = _rows(name, "out", out, tuple(_ACT), dev)
-    _need(w.dim() == 3 and w.dtype in (_I8, torch.uint8) and w.device == dev and
-          w.shape[1] == N and (w.stride(2) == 1 or w.shape[2] == 1), name,
-          f"w must be int8 [E][{N}][K] with adjacent columns on {dev}, got {w.dtype} "
-          f"{tuple(w.shape)} {w.stride()} on {w.device}")
+    f, dev, act = "moe_i8_linear", _gpu("moe_i8_linear", a), _act_code("moe_i8_linear", "out", out)
+    R, Ka, lda = _rows(f, "a", a, _I8, dev)
+    M, N, ldo = _rows(f, "out", out, out.dtype, dev)
+    if w.dim() != 3 or w.dtype not in (_I8, _U8) or w.get_device() != dev or w.shape[1] != N or \
+            (w.stride(2) != 1 and w.shape[2] > 1):
+        raise MoeError(f"{f}: w must be int8 [E][{N}][K] with adjacent columns on GPU {dev}, got "
+                       f"{w.dtype} {tuple(w.shape)} {w.stride()} on {w.device}")
     E, _, K = w.shape
-    ldw = w.stride(1) if N > 1 else (w.stride(0) if E > 1 else max(w.stride(1), K))
-    _need(E == 1 or w.stride(0) == N * ldw, name, "the experts' matrices must lie one after another")
-    _need(w.untyped_storage().nbytes() - w.storage_offset() >= E * N * ldw, name,
-          "the last row of w must reach its stride")
-    _need(Ka >= moe_i8_stride(K), name, f"a must have rows of at least {moe_i8_stride(K)} values")
-    _dense(name, "a_scale", a_scale, (_F32,), R, dev)
-    if w_scale is not None:
-        _dense(name, "w_scale", w_scale, (_F32,), E * N, dev)
-    if row_src is not None:
-        _dense(name, "row_src", row_src, (_I32,), M, dev)
-    _experts(name, offsets, E, dev)
-    d = I8Dims(M, N, K, E, _ACT[out.dtype])
-    _call(name, dev, LIB.moe_i8_linear,
-          (ctypes.byref(d), _p(a), lda, _p(a_scale), R, _p(row_src), row_div, _p(offsets), _p(w),
-           ldw, _p(w_scale), _p(out), ldo), stream)
+    es, ldw, _ = w.stride()
+    if N == 1:
+        ldw = es if E > 1 else max(ldw, K)
+    if E > 1 and es != N * ldw:
+        raise MoeError(f"{f}: the experts' matrices must lie one after another")
+    if w.untyped_storage().nbytes() - w.storage_offset() < E * N * ldw:
+        raise MoeError(f"{f}: the last row of w must reach its stride")
+    if Ka < moe_i8_stride(K):
+        raise MoeError(f"{f}: a must have rows of at least {moe_i8_stride(K)} values")
+    _call(f, dev, LIB.moe_i8_linear,
+          (I8Dims(M, N, K, E, act), a.data_ptr(), lda,
+           _dense(f, "a_scale", a_scale, _F32, R, dev), R,
+           _opt(f, "row_src", row_src, _I32, M, dev), row_div,
+           _opt(f, "offsets", offsets, _I32, E + 1, dev), w.data_ptr(), ldw,
+           _opt(f, "w_scale", w_scale, _F32, E * N, dev), out.data_ptr(), ldo), stream)

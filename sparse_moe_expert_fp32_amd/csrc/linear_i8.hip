@@ -5,6 +5,7 @@
 // The sums are exact in int32 (K <= 65536); the two scales are applied in
 // float32 and the result is rounded once to the output type.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "kernels.h"
@@ -16,73 +17,270 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
 // D = A(16x64) B(64x16) + C in int32: lane l holds A row l%16 / B column l%16
 // with 16 consecutive K bytes of lane group l/16; D lane l holds column l%16,
-// rows 4 (l/16) .. + 3.
+// rows 4 (l/16) .. + 3.  The products run with the matrix w as A and the rows
+// as B, so that a lane ends with 4 adjacent output channels of one row.
 DEV i32x4_t mfma_i8(uint4 a, uint4 b, i32x4_t c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a),
                                                __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
 }
 
-// One 64-row x 64-channel tile per block of 4 waves, each wave 16 rows.
-// blockIdx.y counts the tiles of the experts in order.
-template <typename T>
-__global__ __launch_bounds__(256) void linear_i8_kernel(LinearI8Args A) {
-  __shared__ int tile[2];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, lr = lane & 15, lg = lane >> 4;
-  if (tid == 0) {
-    int left = blockIdx.y, e = 0;
-    tile[0] = -1;
-    for (; e < A.E; ++e) {
-      const int lo = A.offsets ? min(max(A.offsets[e], 0), A.M) : 0;
-      const int hi = A.offsets ? min(A.offsets[e + 1], A.M) : A.M;
-      const int n = hi > lo ? (hi - lo + 63) / 64 : 0;
-      if (left < n) {
-        tile[0] = e;
-        tile[1] = lo + 64 * left;
-        break;
-      }
-      left -= n;
+// Inclusive sum over the lanes of a wave (DPP: within rows of 16, then the
+// row totals passed on).
+DEV int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31
+  return v;
+}
+
+// The tile number `t` in a list that gives every expert ceil(rows / BM)
+// tiles: its expert, first row and the end of the expert's rows.  Offsets are
+// held inside [0, M].  The whole wave asks for the same tile; lane l holds the
+// experts l, l + 64, .. (E <= 64 NC; coalesced loads, all in flight at once),
+// and the list runs over the lanes: one scan over the lanes' sums finds the
+// lane, its experts are then walked.  false: there are fewer tiles.
+struct RowTile { int e, p0, end; };
+template <int BM, int NC> DEV bool find_tile(const int32_t *offsets, int E, int M, int t, RowTile &R) {
+  if (!offsets) {
+    R = RowTile{0, t * BM, M};
+    return t * BM < M;
+  }
+  // (opaque: nothing of this search is kept in registers for the next one)
+  const int lane = (int)opaque(threadIdx.x & 63);
+  int lo[NC], hi[NC], sum = 0;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    lo[i] = offsets[(unsigned)min(64 * i + lane, E)];
+    hi[i] = offsets[(unsigned)min(64 * i + lane + 1, E)];
+  }
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    lo[i] = min(max(lo[i], 0), M);
+    hi[i] = min(max(hi[i], lo[i]), M);
+    sum += (hi[i] - lo[i] + BM - 1) / BM;   // (0 behind the last expert)
+  }
+  const int upto = wave_scan(sum);
+  const int src = __popcll(__ballot(upto <= t));   // lanes whose tiles end before t
+  if (src >= 64) return false;
+  int left = t - __builtin_amdgcn_readlane(upto - sum, src);
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int l = __builtin_amdgcn_readlane(lo[i], src);
+    const int h = __builtin_amdgcn_readlane(hi[i], src);
+    const int n = (h - l + BM - 1) / BM;
+    if (!found && left < n) {
+      found = true;
+      R = RowTile{64 * i + src, l + BM * left, h};
+    }
+    left -= n;
+  }
+  return found;
+}
+
+// The row of a that row p of the product reads (kept inside a).
+DEV int source_row(const LinearI8Args &A, int p) {
+  return min(max(A.row_src ? A.row_src[p] / A.row_div : p, 0), A.a_rows - 1);
+}
+
+DEV uint4 ld16(const int8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
+
+template <typename T> DEV void put4(T *p, bool vec, int n, int N, const float *v) {
+  if (vec && n + 3 < N) {
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint2 *>(p) = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
+    else
+      *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (n + i < N) {
+      if constexpr (sizeof(T) == 2) p[i] = (uint16_t)cvt_pk_bf16(v[i], v[i]);
+      else p[i] = v[i];
     }
   }
-  __syncthreads();
-  const int e = tile[0], p0 = tile[1];
-  if (e < 0) return;
-  const int end = A.offsets ? min(A.offsets[e + 1], A.M) : A.M;
-  const int n0 = blockIdx.x * 64;
-  const int p = p0 + 16 * w + lr, pc = min(p, end - 1);
-  const int r = min(max(A.row_src ? A.row_src[pc] / A.row_div : pc, 0), A.a_rows - 1);
-  const int8_t *ap = A.a + (size_t)r * A.lda;
-  const int8_t *wp[4];
+}
+
+// ---- few rows per matrix: bound by reading the matrices once.
+//
+// A block takes 16 MF rows (one tile of the list) and a range of output
+// channels in fragments of 16.  The rows go into LDS once, in the order in
+// which the matrix instructions read them (fragment m, step s of 64: 1 KB,
+// lane after lane; rows too long for that are read from memory each time).
+// The matrix goes straight into registers: a wave keeps the next D steps in
+// flight while it multiplies the current D, across fragments, without a
+// barrier.  KS = 1: every wave has fragments of its own.  KS = NW: the waves
+// share the fragments and split the steps (wave w takes steps w, w + NW, ..),
+// their sums are added through LDS; for launches with too few fragments to
+// give every wave one.
+template <typename T, int MF, int NW, int KS, int D, int NC, bool ALDS>
+__global__ __launch_bounds__(64 * NW) void linear_i8_short_kernel(LinearI8Args A, int per) {
+  constexpr int BM = 16 * MF, FW = NW / KS;
+  extern __shared__ __attribute__((aligned(16))) int8_t lds_a[];
+  __shared__ __attribute__((aligned(16))) int red[KS > 1 ? KS * MF * 256 : 4];
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int fw = KS > 1 ? 0 : w, kw = KS > 1 ? w : 0;
+  const int steps = (A.K + 63) >> 6, nfr = (A.N + 15) >> 4;
+  const int ns = (steps - kw + KS - 1) / KS, groups = (ns + D - 1) / D;
+  const int f0 = blockIdx.x * FW * per + fw;
+  const int cnt = max(0, min(per, (nfr - f0 + FW - 1) / FW));
+  const int ldw = (int)A.ldw;
+  const bool vec = (((uintptr_t)A.out & (4 * sizeof(T) - 1)) | (A.ldo & 3)) == 0;
+
+  RowTile R;
+  for (int t = blockIdx.y; find_tile<BM, NC>(A.offsets, A.E, A.M, t, R); t += gridDim.y) {
+    const int8_t *we = A.w + (size_t)R.e * A.N * A.ldw;
+    // steps D g .. D g + D - 1 of this wave's fragment i (the last one again
+    // behind the end: read twice, not used)
+    uint4 ring[D];
+    auto column = [&](int i) {
+      return we + (size_t)min(16 * (f0 + FW * i) + lr, A.N - 1) * A.ldw;
+    };
+    auto at_step = [&](int s) { return min(64 * (kw + KS * min(s, ns - 1)) + 16 * lg, ldw - 16); };
+    if (cnt > 0 && ns > 0) {
+      const int8_t *c = column(0);
 #pragma unroll
-  for (int f = 0; f < 4; ++f)
-    wp[f] = A.w + ((size_t)e * A.N + min(n0 + 16 * f + lr, A.N - 1)) * A.ldw;
-  i32x4_t acc[4] = {};
-  for (int k = 16 * lg; k < ((A.K + 63) & ~63); k += 64) {
-    const uint4 av = *reinterpret_cast<const uint4 *>(ap + k);
-    const int kw = min(k, (int)A.ldw - 16);
-#pragma unroll
-    for (int f = 0; f < 4; ++f)
-      acc[f] = mfma_i8(*reinterpret_cast<const uint4 *>(wp[f] + kw), av, acc[f]);
-  }
-  if (p >= end) return;
-  const float sa = A.a_scale[r];
-  T *out = (T *)A.out + (size_t)p * A.ldo;
-#pragma unroll
-  for (int f = 0; f < 4; ++f)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + 16 * f + 4 * lg + i;
-      if (n < A.N) {
-        const float sw = A.w_scale ? A.w_scale[(size_t)e * A.N + n] : 1.0f;
-        Elem<T>::st(out, n, (float)acc[f][i] * (sa * sw));
-      }
+      for (int j = 0; j < D; ++j) ring[j] = ld16(c + at_step(j));
     }
+    int rows[MF];
+    float sa[MF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+      rows[m] = source_row(A, min(R.p0 + 16 * m + lr, R.end - 1));
+      sa[m] = A.a_scale[rows[m]];
+    }
+    if constexpr (ALDS) {
+      // (what stands in the places of rows behind the end reaches only those
+      // rows' sums, which are not stored)
+      for (int s = w; s < steps; s += NW) {
+        uint4 v[MF];
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+          if (R.p0 + 16 * m + lr < R.end)
+            v[m] = ld16(A.a + (size_t)rows[m] * A.lda + 64 * s + 16 * lg);
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+          if (R.p0 + 16 * m + lr < R.end)
+            *reinterpret_cast<uint4 *>(lds_a + ((m * steps + s) * 64 + lane) * 16) = v[m];
+      }
+      __syncthreads();
+    }
+    for (int i = 0; i < cnt; ++i) {
+      // the channels' scales, asked for before the next steps of the matrix
+      const int n = 16 * (f0 + FW * i) + 4 * lg;
+      const float *ws = A.w_scale ? A.w_scale + (size_t)R.e * A.N : A.a_scale;
+      float sw[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sw[c] = ws[A.w_scale ? min(n + c, A.N - 1) : 0];
+      i32x4_t acc[MF] = {};
+      auto group = [&](int g, auto prefetch) {
+        constexpr bool PF = decltype(prefetch)::value;
+        const bool wrap = g + 1 == groups;
+        const int8_t *nc = PF ? column(wrap ? i + 1 : i) : nullptr;
+        const int ng = wrap ? 0 : g + 1;
+#pragma unroll
+        for (int j = 0; j < D; ++j) {
+          const int s = g * D + j;
+          if (s < ns) {
+            const int sk = kw + KS * s;
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+              uint4 av;
+              if constexpr (ALDS)
+                av = *reinterpret_cast<const uint4 *>(lds_a + ((m * steps + sk) * 64 + lane) * 16);
+              else
+                av = ld16(A.a + (size_t)rows[m] * A.lda + 64 * sk + 16 * lg);
+              acc[m] = mfma_i8(ring[j], av, acc[m]);
+            }
+          }
+          if constexpr (PF) ring[j] = ld16(nc + at_step(ng * D + j));
+        }
+      };
+      for (int g = 0; g < groups; ++g) {
+        if (g + 1 < groups || i + 1 < cnt) group(g, std::true_type{});
+        else group(g, std::false_type{});
+      }
+      if constexpr (KS > 1) {
+        i32x4_t *rv = reinterpret_cast<i32x4_t *>(red);
+#pragma unroll
+        for (int m = 0; m < MF; ++m) rv[(w * MF + m) * 64 + lane] = acc[m];
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+          if (m % KS != w) continue;   // fragment m is added by wave m % KS
+#pragma unroll
+          for (int o = 1; o < KS; ++o) acc[m] += rv[(((w + o) % KS) * MF + m) * 64 + lane];
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MF; ++m) {
+        if (KS > 1 && m % KS != w) continue;
+        const int p = R.p0 + 16 * m + lr;
+        if (p >= R.end || n >= A.N) continue;
+        float v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = (float)acc[m][c] * (sa[m] * (A.w_scale ? sw[c] : 1.0f));
+        put4<T>((T *)A.out + (size_t)p * A.ldo + n, vec, n, A.N, v);
+      }
+      if constexpr (KS > 1) __syncthreads();   // the sums are read before the next ones are written
+    }
+    if constexpr (ALDS) __syncthreads();       // and the rows before the next tile's
+  }
+}
+
+// Short launches: rows per tile from the average rows of a matrix (each tile
+// reads its matrix once; more rows a tile cost LDS, fewer read the matrix
+// again), the waves' share from the number of fragments.
+template <typename T, int MF, int NW> static void launch_short(const LinearI8Args &A, hipStream_t st) {
+  constexpr int BM = 16 * MF;
+  const int steps = (A.K + 63) / 64, nfr = (A.N + 15) / 16;
+  // at most one tile more than M / BM per expert, and none without a row
+  const int tiles = A.offsets ? std::min(A.M, A.M / BM + A.E) : (A.M + BM - 1) / BM;
+  const size_t lds = (size_t)BM * steps * 64;
+  const bool alds = lds <= 128 * 1024;
+  // enough waves to ask every CU for several blocks' worth of the matrix
+  const bool split = (int64_t)nfr * tiles < 4096;
+  const int ns = split ? (steps + NW - 1) / NW : steps;
+  const int per = split ? (nfr * tiles + 1023) / 1024 : (int)std::max<int64_t>(1, std::min<int64_t>(
+      nfr / NW, ((int64_t)nfr * tiles + NW * 1024 - 1) / (NW * 1024)));
+  dim3 grid(((nfr + per - 1) / per + (split ? 1 : NW) - 1) / (split ? 1 : NW), std::min(tiles, 32768));
+  // steps in flight: the depth that leaves the fewest empty places
+  const int pad8 = (ns + 7) / 8 * 8 - ns, pad12 = (ns + 11) / 12 * 12 - ns;
+  const int depth = ns <= 4 ? 4 : ns <= 8 ? 8 : pad12 < pad8 ? 12 : ns >= 16 && ns % 16 == 0 ? 16 : 8;
+#define MOE_L(KS, D, NC, AL) \
+  linear_i8_short_kernel<T, MF, NW, KS, D, NC, AL><<<grid, 64 * NW, AL ? lds : 0, st>>>(A, per)
+#define MOE_LE(KS, D)                            \
+  if (A.E <= 64) MOE_L(KS, D, 1, true);          \
+  else MOE_L(KS, D, 16, true);
+  if (!alds) {
+    if (split) MOE_L(NW, 8, 16, false);
+    else MOE_L(1, 8, 16, false);
+  } else if (split) {
+    if (ns <= 4) { MOE_LE(NW, 4) } else { MOE_LE(NW, 8) }
+  } else if (depth == 4) { MOE_LE(1, 4)
+  } else if (depth == 8) { MOE_LE(1, 8)
+  } else if (depth == 12) { MOE_LE(1, 12)
+  } else { MOE_LE(1, 16) }
+#undef MOE_LE
+#undef MOE_L
 }
 
 void launch_linear_i8(bool bf16, const LinearI8Args &A, hipStream_t st) {
-  const int tiles = (A.M + 63) / 64 + (A.offsets ? A.E : 0);
-  dim3 grid((A.N + 63) / 64, tiles);
-  if (bf16) linear_i8_kernel<bf16_t><<<grid, 256, 0, st>>>(A);
-  else linear_i8_kernel<float><<<grid, 256, 0, st>>>(A);
+  const int avg = A.M / A.E;
+  if (bf16) {
+    if (avg <= 8) launch_short<bf16_t, 1, 4>(A, st);
+    else if (avg <= 24) launch_short<bf16_t, 2, 4>(A, st);
+    else launch_short<bf16_t, 4, 8>(A, st);
+  } else {
+    if (avg <= 8) launch_short<float, 1, 4>(A, st);
+    else if (avg <= 24) launch_short<float, 2, 4>(A, st);
+    else launch_short<float, 4, 8>(A, st);
+  }
 }
 
 }  // namespace moe

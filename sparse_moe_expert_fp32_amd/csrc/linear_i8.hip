@@ -36,50 +36,61 @@ DEV int wave_scan(int v) {
   return v;
 }
 
-// The tile number `t` in a list that gives every expert ceil(rows / BM)
-// tiles: its expert, first row and the end of the expert's rows.  Offsets are
-// held inside [0, M].  The whole wave asks for the same tile; lane l holds the
-// experts l, l + 64, .. (E <= 64 NC; coalesced loads, all in flight at once),
-// and the list runs over the lanes: one scan over the lanes' sums finds the
-// lane, its experts are then walked.  false: there are fewer tiles.
+// The list of row tiles, ceil(rows / BM) for every expert, as a wave holds it:
+// lane l has the experts l, l + 64, .. (E <= 64 NC; offsets held inside
+// [0, M], loads coalesced and all in flight at once), and the list runs over
+// the lanes.  One scan over the lanes' sums finds the lane of a tile, whose
+// experts are then walked.  The whole wave asks for the same tile.
 struct RowTile { int e, p0, end; };
-template <int BM, int NC> DEV bool find_tile(const int32_t *offsets, int E, int M, int t, RowTile &R) {
-  if (!offsets) {
-    R = RowTile{0, t * BM, M};
-    return t * BM < M;
-  }
-  // (opaque: nothing of this search is kept in registers for the next one)
-  const int lane = (int)opaque(threadIdx.x & 63);
-  int lo[NC], hi[NC], sum = 0;
+template <int BM, int NC> struct TileList {
+  int lo[NC], hi[NC], sum, upto, M;
+  bool all;   // one matrix for every row
+
+  DEV TileList(const int32_t *offsets, int E, int M_) : M(M_), all(!offsets) {
+    if (all) return;
+    // (opaque: nothing of this is kept in registers for the next search)
+    const int lane = (int)opaque(threadIdx.x & 63);
+    sum = 0;
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    lo[i] = offsets[(unsigned)min(64 * i + lane, E)];
-    hi[i] = offsets[(unsigned)min(64 * i + lane + 1, E)];
-  }
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    lo[i] = min(max(lo[i], 0), M);
-    hi[i] = min(max(hi[i], lo[i]), M);
-    sum += (hi[i] - lo[i] + BM - 1) / BM;   // (0 behind the last expert)
-  }
-  const int upto = wave_scan(sum);
-  const int src = __popcll(__ballot(upto <= t));   // lanes whose tiles end before t
-  if (src >= 64) return false;
-  int left = t - __builtin_amdgcn_readlane(upto - sum, src);
-  bool found = false;
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int l = __builtin_amdgcn_readlane(lo[i], src);
-    const int h = __builtin_amdgcn_readlane(hi[i], src);
-    const int n = (h - l + BM - 1) / BM;
-    if (!found && left < n) {
-      found = true;
-      R = RowTile{64 * i + src, l + BM * left, h};
+    for (int i = 0; i < NC; ++i) {
+      lo[i] = offsets[(unsigned)min(64 * i + lane, E)];
+      hi[i] = offsets[(unsigned)min(64 * i + lane + 1, E)];
     }
-    left -= n;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      lo[i] = min(max(lo[i], 0), M);
+      hi[i] = min(max(hi[i], lo[i]), M);
+      sum += (hi[i] - lo[i] + BM - 1) / BM;   // (0 behind the last expert)
+    }
+    upto = wave_scan(sum);
   }
-  return found;
-}
+  DEV int count() const {
+    return all ? (M + BM - 1) / BM : __builtin_amdgcn_readlane(upto, 63);
+  }
+  // tile t (false: there are fewer)
+  DEV bool get(int t, RowTile &R) const {
+    if (all) {
+      R = RowTile{0, t * BM, M};
+      return t * BM < M;
+    }
+    const int src = __popcll(__ballot(upto <= t));   // lanes whose tiles end before t
+    if (src >= 64) return false;
+    int left = t - __builtin_amdgcn_readlane(upto - sum, src);
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int l = __builtin_amdgcn_readlane(lo[i], src);
+      const int h = __builtin_amdgcn_readlane(hi[i], src);
+      const int n = (h - l + BM - 1) / BM;
+      if (!found && left < n) {
+        found = true;
+        R = RowTile{64 * i + src, l + BM * left, h};
+      }
+      left -= n;
+    }
+    return found;
+  }
+};
 
 // The row of a that row p of the product reads (kept inside a).
 DEV int source_row(const LinearI8Args &A, int p) {
@@ -133,7 +144,7 @@ __global__ __launch_bounds__(64 * NW) void linear_i8_short_kernel(LinearI8Args A
   const bool vec = (((uintptr_t)A.out & (4 * sizeof(T) - 1)) | (A.ldo & 3)) == 0;
 
   RowTile R;
-  for (int t = blockIdx.y; find_tile<BM, NC>(A.offsets, A.E, A.M, t, R); t += gridDim.y) {
+  for (int t = blockIdx.y; TileList<BM, NC>(A.offsets, A.E, A.M).get(t, R); t += gridDim.y) {
     const int8_t *we = A.w + (size_t)R.e * A.N * A.ldw;
     // steps D g .. D g + D - 1 of this wave's fragment i (the last one again
     // behind the end: read twice, not used)
@@ -270,17 +281,180 @@ template <typename T, int MF, int NW> static void launch_short(const LinearI8Arg
 #undef MOE_L
 }
 
-void launch_linear_i8(bool bf16, const LinearI8Args &A, hipStream_t st) {
-  const int avg = A.M / A.E;
-  if (bf16) {
-    if (avg <= 8) launch_short<bf16_t, 1, 4>(A, st);
-    else if (avg <= 24) launch_short<bf16_t, 2, 4>(A, st);
-    else launch_short<bf16_t, 4, 8>(A, st);
-  } else {
-    if (avg <= 8) launch_short<float, 1, 4>(A, st);
-    else if (avg <= 24) launch_short<float, 2, 4>(A, st);
-    else launch_short<float, 4, 8>(A, st);
+// ---- many rows per matrix: tiles of up to 256 rows x 128 channels, two
+// blocks of four waves per CU (2 x 2 waves, each half of the rows in
+// interleaved fragments of 16 and 64 channels), steps of 64 along K through
+// two LDS slots.  A step goes from memory into registers two steps before it
+// is written to LDS (the matrix comes from HBM: its latency is the reason),
+// and the other block on the CU multiplies meanwhile.  MI: 16-row fragments a
+// wave has (32 MI rows); a tile runs as the smallest class that holds its rows.
+constexpr int BG_BM = 256, BG_BN = 128, BG_KS = 64;
+constexpr int BG_SLOT = (BG_BM + BG_BN) * BG_KS;   // bytes of one LDS slot
+
+// Rows of 64 bytes in LDS.  Chunk c (16 bytes) of row r stands at place
+// c ^ (r >> 2) & 3 for the rows of a, whose fragments read 16 adjacent rows,
+// and at c ^ (r >> 3) & 3 for the channels, whose fragments read the rows
+// gt_col(f, 0..15): either way 16 lanes reading one chunk touch every bank
+// once.  Both places are the same for every fragment of a wave and every
+// piece of a thread, so that all addresses are one base and a constant.
+constexpr int kWaitLds = 0xC07F;   // s_waitcnt lgkmcnt(0), nothing else
+
+template <typename T, int MI>
+DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds) {
+  constexpr int RP = (MI + 1) / 2;   // 16-byte pieces of a step's rows per thread
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
+  const int w = tid >> 6, wm = w & 1, wn = w >> 1;
+  const int tr = tid >> 2, tc = tid & 3;
+  const int steps = 2 * ((A.K + 2 * BG_KS - 1) / (2 * BG_KS));   // (rows of a hold 0 behind K)
+  const int a_put = tr * BG_KS + ((tc ^ (tr >> 2)) & 3) * 16;
+  const int w_put = BG_BM * BG_KS + tr * BG_KS + ((tc ^ (tr >> 3)) & 3) * 16;
+  const int a_get = (16 * wm + lr) * BG_KS + ((lg ^ (lr >> 2)) & 3) * 16;
+  const int w_get = BG_BM * BG_KS + (64 * wn + gt_col(0, lr)) * BG_KS + ((lg ^ (lr >> 2)) & 3) * 16;
+  const int8_t *ap[RP], *wp[2];
+#pragma unroll
+  for (int i = 0; i < RP; ++i)
+    ap[i] = A.a + (size_t)source_row(A, min(R.p0 + tr + 64 * i, R.end - 1)) * A.lda + 16 * tc;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    wp[i] = A.w + ((size_t)R.e * A.N + min(n0 + tr + 64 * i, A.N - 1)) * A.ldw;
+  struct Stage { uint4 a[RP], w[2]; };
+  auto load = [&](Stage &S, int s) {
+    const int k = BG_KS * min(s, steps - 1), kw = min(k + 16 * tc, (int)A.ldw - 16);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) S.w[i] = ld16(wp[i] + kw);
+#pragma unroll
+    for (int i = 0; i < RP; ++i) S.a[i] = ld16(ap[i] + k);
+  };
+  auto store = [&](const Stage &S, uint8_t *slot) {
+#pragma unroll
+    for (int i = 0; i < RP; ++i)
+      *reinterpret_cast<uint4 *>(slot + a_put + 64 * BG_KS * i) = S.a[i];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<uint4 *>(slot + w_put + 64 * BG_KS * i) = S.w[i];
+  };
+  i32x4_t acc[MI][4] = {};
+  auto multiply = [&](const uint8_t *slot) {
+    uint4 wv[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+      wv[f] = *reinterpret_cast<const uint4 *>(slot + w_get + BG_KS * gt_col(f, 0));
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const uint4 av = *reinterpret_cast<const uint4 *>(slot + a_get + 32 * BG_KS * i);
+#pragma unroll
+      for (int f = 0; f < 4; ++f) acc[i][f] = mfma_i8(wv[f], av, acc[i][f]);
+    }
+  };
+  uint8_t *s0 = lds, *s1 = lds + BG_SLOT;
+  Stage P, Q;
+  load(P, 0);
+  load(Q, 1);
+  store(P, s0);
+  load(P, 2);
+  __builtin_amdgcn_s_waitcnt(kWaitLds);
+  block_barrier();
+  for (int j = 0; j < steps; j += 2) {
+    // (the scheduler may not mix the parts: two steps in registers is what fits)
+    multiply(s0);
+    __builtin_amdgcn_sched_barrier(0);
+    store(Q, s1);
+    __builtin_amdgcn_sched_barrier(0);
+    load(Q, j + 3);
+    __builtin_amdgcn_s_waitcnt(kWaitLds);
+    block_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(s1);
+    __builtin_amdgcn_sched_barrier(0);
+    store(P, s0);
+    __builtin_amdgcn_sched_barrier(0);
+    load(P, j + 4);
+    __builtin_amdgcn_s_waitcnt(kWaitLds);
+    block_barrier();
+    __builtin_amdgcn_sched_barrier(0);
   }
+  const bool vec = (((uintptr_t)A.out & 15) | ((A.ldo * sizeof(T)) & 15)) == 0;
+  float sw[4][4];
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int n = n0 + 64 * wn + gt_col(f, 4 * lg) + c;
+      sw[f][c] = A.w_scale ? A.w_scale[(size_t)R.e * A.N + min(n, A.N - 1)] : 1.0f;
+    }
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int p = R.p0 + 16 * (2 * i + wm) + lr;
+    if (p >= R.end) continue;
+    const float sa = A.a_scale[source_row(A, p)];
+    T *out = (T *)A.out + (size_t)p * A.ldo;
+#pragma unroll
+    for (int f = 0; f < 4; f += 2) {   // 8 adjacent channels
+      const int n = n0 + 64 * wn + gt_col(f, 4 * lg);
+      float v[8];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        v[c] = (float)acc[i][f][c] * (sa * sw[f][c]);
+        v[4 + c] = (float)acc[i][f + 1][c] * (sa * sw[f + 1][c]);
+      }
+      if constexpr (sizeof(T) == 2) {
+        if (vec && n + 7 < A.N) {
+          *reinterpret_cast<uint4 *>(out + n) =
+              make_uint4(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]),
+                         cvt_pk_bf16(v[4], v[5]), cvt_pk_bf16(v[6], v[7]));
+          continue;
+        }
+      }
+      put4<T>(out + n, vec, n, A.N, v);
+      put4<T>(out + n + 4, vec, n + 4, A.N, v + 4);
+    }
+  }
+}
+
+// Blocks go round the 8 XCDs in turn; each XCD takes a contiguous run of the
+// (row tile, channel tile) list, so that tiles that share rows and matrices
+// share its L2.  The run is an eighth of the tiles there are, not of the grid.
+template <typename T, int NC>
+__global__ __launch_bounds__(256, 2) void linear_i8_big_kernel(LinearI8Args A) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * BG_SLOT];
+  const int nt = (A.N + BG_BN - 1) / BG_BN;
+  RowTile R;
+  int n0;
+  {
+    const TileList<BG_BM, NC> list(A.offsets, A.E, A.M);
+    const int64_t items = (int64_t)list.count() * nt, run = (items + 7) / 8;
+    const int64_t at = blockIdx.x >> 3, item = run * (blockIdx.x & 7) + at;
+    if (at >= run || item >= items) return;
+    const int t = (int)(item / nt);
+    n0 = (int)(item - (int64_t)t * nt) * BG_BN;
+    if (!list.get(t, R)) return;
+  }
+  const int rows = R.end - R.p0;
+  if (rows <= 64) big_tile<T, 2>(A, R, n0, lds);
+  else if (rows <= 128) big_tile<T, 4>(A, R, n0, lds);
+  else if (rows <= 192) big_tile<T, 6>(A, R, n0, lds);
+  else big_tile<T, 8>(A, R, n0, lds);
+}
+
+template <typename T> static void launch_big(const LinearI8Args &A, hipStream_t st) {
+  const int64_t tiles = A.offsets ? A.M / BG_BM + std::min(A.M, A.E) : (A.M + BG_BM - 1) / BG_BM;
+  const int64_t items = tiles * ((A.N + BG_BN - 1) / BG_BN);
+  const unsigned grid = (unsigned)((items + 7) / 8 * 8);
+  if (A.E <= 64) linear_i8_big_kernel<T, 1><<<grid, 256, 0, st>>>(A);
+  else linear_i8_big_kernel<T, 16><<<grid, 256, 0, st>>>(A);
+}
+
+template <typename T> static void launch_linear(const LinearI8Args &A, hipStream_t st) {
+  const int avg = A.M / A.E;
+  if (avg > 64) launch_big<T>(A, st);
+  else if (avg <= 8) launch_short<T, 1, 4>(A, st);
+  else if (avg <= 24) launch_short<T, 2, 4>(A, st);
+  else launch_short<T, 4, 8>(A, st);
+}
+
+void launch_linear_i8(bool bf16, const LinearI8Args &A, hipStream_t st) {
+  if (bf16) launch_linear<bf16_t>(A, st);
+  else launch_linear<float>(A, st);
 }
 
 }  // namespace moe

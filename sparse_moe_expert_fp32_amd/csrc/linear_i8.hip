@@ -283,93 +283,82 @@ template <typename T, int MF, int NW> static void launch_short(const LinearI8Arg
 
 // ---- many rows per matrix: tiles of up to 256 rows x 128 channels, two
 // blocks of four waves per CU (2 x 2 waves, each half of the rows in
-// interleaved fragments of 16 and 64 channels), steps of 64 along K through
-// two LDS slots.  A step goes from memory into registers two steps before it
-// is written to LDS (the matrix comes from HBM: its latency is the reason),
-// and the other block on the CU multiplies meanwhile.  MI: 16-row fragments a
-// wave has (32 MI rows); a tile runs as the smallest class that holds its rows.
-constexpr int BG_BM = 256, BG_BN = 128, BG_KS = 64;
-constexpr int BG_SLOT = (BG_BM + BG_BN) * BG_KS;   // bytes of one LDS slot
+// interleaved fragments of 16 and 64 channels), steps of 128 along K, so that
+// a row's share of a step is a whole 128-byte line.  A step goes from memory
+// into registers while the one before it is multiplied from LDS; one block of
+// the CU multiplies while the other one writes LDS or waits.  MI: 16-row
+// fragments a wave has (32 MI rows); a tile runs as the smallest class that
+// holds its rows.
+constexpr int BG_BM = 256, BG_BN = 128, BG_KS = 128;
+constexpr int BG_A = BG_BM * BG_KS, BG_LDS = BG_A + BG_BN * BG_KS;   // bytes
 
-// Rows of 64 bytes in LDS.  Chunk c (16 bytes) of row r stands at place
-// c ^ (r >> 2) & 3 for the rows of a, whose fragments read 16 adjacent rows,
-// and at c ^ (r >> 3) & 3 for the channels, whose fragments read the rows
-// gt_col(f, 0..15): either way 16 lanes reading one chunk touch every bank
-// once.  Both places are the same for every fragment of a wave and every
-// piece of a thread, so that all addresses are one base and a constant.
+// Rows of 128 bytes in LDS.  Chunk c (16 bytes) of row r stands at place
+// c ^ (r >> 1) & 7 for the rows of a, whose fragments read 16 adjacent rows,
+// and at c ^ (2 (r >> 3 & 3) + (r >> 1 & 1)) for the channels, whose fragments
+// read the rows gt_col(f, 0..15): either way 16 lanes reading one chunk touch
+// every bank once.  The places are the same for every fragment of a wave and
+// every piece of a thread, so that all addresses are a base and a constant.
+DEV int bg_swz_a(int r) { return (r >> 1) & 7; }
+DEV int bg_swz_w(int r) { return ((r >> 2) & 6) | ((r >> 1) & 1); }
+
 constexpr int kWaitLds = 0xC07F;   // s_waitcnt lgkmcnt(0), nothing else
 
 template <typename T, int MI>
 DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds) {
-  constexpr int RP = (MI + 1) / 2;   // 16-byte pieces of a step's rows per thread
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
   const int w = tid >> 6, wm = w & 1, wn = w >> 1;
-  const int tr = tid >> 2, tc = tid & 3;
-  const int steps = 2 * ((A.K + 2 * BG_KS - 1) / (2 * BG_KS));   // (rows of a hold 0 behind K)
-  const int a_put = tr * BG_KS + ((tc ^ (tr >> 2)) & 3) * 16;
-  const int w_put = BG_BM * BG_KS + tr * BG_KS + ((tc ^ (tr >> 3)) & 3) * 16;
-  const int a_get = (16 * wm + lr) * BG_KS + ((lg ^ (lr >> 2)) & 3) * 16;
-  const int w_get = BG_BM * BG_KS + (64 * wn + gt_col(0, lr)) * BG_KS + ((lg ^ (lr >> 2)) & 3) * 16;
-  const int8_t *ap[RP], *wp[2];
+  const int tr = tid >> 3, tc = tid & 7;     // row and chunk of this thread's first piece
+  const int steps = (A.K + BG_KS - 1) / BG_KS;   // (rows of a hold 0 behind K)
+  const int a_put = tr * BG_KS + (tc ^ bg_swz_a(tr)) * 16;
+  const int w_put = BG_A + tr * BG_KS + (tc ^ bg_swz_w(tr)) * 16;
+  const int ar = 16 * wm + lr, wr = 64 * wn + gt_col(0, lr);
+  const int a_get = ar * BG_KS + (lg ^ bg_swz_a(ar)) * 16;
+  const int w_get = BG_A + wr * BG_KS + (lg ^ bg_swz_w(wr)) * 16;
+  const int8_t *ap[MI], *wp[4];
 #pragma unroll
-  for (int i = 0; i < RP; ++i)
-    ap[i] = A.a + (size_t)source_row(A, min(R.p0 + tr + 64 * i, R.end - 1)) * A.lda + 16 * tc;
+  for (int i = 0; i < MI; ++i)
+    ap[i] = A.a + (size_t)source_row(A, min(R.p0 + tr + 32 * i, R.end - 1)) * A.lda + 16 * tc;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    wp[i] = A.w + ((size_t)R.e * A.N + min(n0 + tr + 64 * i, A.N - 1)) * A.ldw;
-  struct Stage { uint4 a[RP], w[2]; };
-  auto load = [&](Stage &S, int s) {
+  for (int i = 0; i < 4; ++i)
+    wp[i] = A.w + ((size_t)R.e * A.N + min(n0 + tr + 32 * i, A.N - 1)) * A.ldw;
+  uint4 sa_[MI], sw_[4];   // the step on its way
+  auto load = [&](int s) {
     const int k = BG_KS * min(s, steps - 1), kw = min(k + 16 * tc, (int)A.ldw - 16);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) S.w[i] = ld16(wp[i] + kw);
+    for (int i = 0; i < 4; ++i) sw_[i] = ld16(wp[i] + kw);
 #pragma unroll
-    for (int i = 0; i < RP; ++i) S.a[i] = ld16(ap[i] + k);
+    for (int i = 0; i < MI; ++i) sa_[i] = ld16(ap[i] + k);
   };
-  auto store = [&](const Stage &S, uint8_t *slot) {
+  auto store = [&]() {
 #pragma unroll
-    for (int i = 0; i < RP; ++i)
-      *reinterpret_cast<uint4 *>(slot + a_put + 64 * BG_KS * i) = S.a[i];
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4 *>(lds + w_put + 32 * BG_KS * i) = sw_[i];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<uint4 *>(slot + w_put + 64 * BG_KS * i) = S.w[i];
+    for (int i = 0; i < MI; ++i)
+      *reinterpret_cast<uint4 *>(lds + a_put + 32 * BG_KS * i) = sa_[i];
   };
   i32x4_t acc[MI][4] = {};
-  auto multiply = [&](const uint8_t *slot) {
+  auto multiply = [&](int h) {   // K 64 h .. 64 h + 63 of the step: chunks 4 h + lg
     uint4 wv[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f)
-      wv[f] = *reinterpret_cast<const uint4 *>(slot + w_get + BG_KS * gt_col(f, 0));
+      wv[f] = *reinterpret_cast<const uint4 *>(lds + (w_get ^ (64 * h)) + BG_KS * gt_col(f, 0));
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const uint4 av = *reinterpret_cast<const uint4 *>(slot + a_get + 32 * BG_KS * i);
+      const uint4 av = *reinterpret_cast<const uint4 *>(lds + (a_get ^ (64 * h)) + 32 * BG_KS * i);
 #pragma unroll
       for (int f = 0; f < 4; ++f) acc[i][f] = mfma_i8(wv[f], av, acc[i][f]);
     }
   };
-  uint8_t *s0 = lds, *s1 = lds + BG_SLOT;
-  Stage P, Q;
-  load(P, 0);
-  load(Q, 1);
-  store(P, s0);
-  load(P, 2);
-  __builtin_amdgcn_s_waitcnt(kWaitLds);
-  block_barrier();
-  for (int j = 0; j < steps; j += 2) {
-    // (the scheduler may not mix the parts: two steps in registers is what fits)
-    multiply(s0);
-    __builtin_amdgcn_sched_barrier(0);
-    store(Q, s1);
-    __builtin_amdgcn_sched_barrier(0);
-    load(Q, j + 3);
+  load(0);
+  for (int j = 0; j < steps; ++j) {
+    store();
+    __builtin_amdgcn_sched_barrier(0);   // (the registers are free again)
+    load(j + 1);
     __builtin_amdgcn_s_waitcnt(kWaitLds);
     block_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(s1);
-    __builtin_amdgcn_sched_barrier(0);
-    store(P, s0);
-    __builtin_amdgcn_sched_barrier(0);
-    load(P, j + 4);
-    __builtin_amdgcn_s_waitcnt(kWaitLds);
+    multiply(0);
+    multiply(1);
     block_barrier();
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -416,7 +405,7 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
 // share its L2.  The run is an eighth of the tiles there are, not of the grid.
 template <typename T, int NC>
 __global__ __launch_bounds__(256, 2) void linear_i8_big_kernel(LinearI8Args A) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * BG_SLOT];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[BG_LDS];
   const int nt = (A.N + BG_BN - 1) / BG_BN;
   RowTile R;
   int n0;

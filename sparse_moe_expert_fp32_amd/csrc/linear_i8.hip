@@ -314,20 +314,24 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
   const int ar = 16 * wm + lr, wr = 64 * wn + gt_col(0, lr);
   const int a_get = ar * BG_KS + (lg ^ bg_swz_a(ar)) * 16;
   const int w_get = BG_A + wr * BG_KS + (lg ^ bg_swz_w(wr)) * 16;
-  const int8_t *ap[MI], *wp[4];
+  // byte offsets inside a and inside the matrix are below 2^32 (launch_linear)
+  const int8_t *we = A.w + (size_t)R.e * A.N * A.ldw;
+  uint32_t ao[MI], wo[4];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
-    ap[i] = A.a + (size_t)source_row(A, min(R.p0 + tr + 32 * i, R.end - 1)) * A.lda + 16 * tc;
+    ao[i] = (uint32_t)source_row(A, min(R.p0 + tr + 32 * i, R.end - 1)) * (uint32_t)A.lda + 16 * tc;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    wp[i] = A.w + ((size_t)R.e * A.N + min(n0 + tr + 32 * i, A.N - 1)) * A.ldw;
+    wo[i] = (uint32_t)min(n0 + tr + 32 * i, A.N - 1) * (uint32_t)A.ldw;
   uint4 sa_[MI], sw_[4];   // the step on its way
   auto load = [&](int s) {
-    const int k = BG_KS * min(s, steps - 1), kw = min(k + 16 * tc, (int)A.ldw - 16);
+    const int k = BG_KS * min(s, steps - 1);
+    const uint32_t kw = (uint32_t)min(k + 16 * tc, (int)A.ldw - 16);
+    const int8_t *ak = A.a + k;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sw_[i] = ld16(wp[i] + kw);
+    for (int i = 0; i < 4; ++i) sw_[i] = ld16(we + (size_t)(wo[i] + kw));
 #pragma unroll
-    for (int i = 0; i < MI; ++i) sa_[i] = ld16(ap[i] + k);
+    for (int i = 0; i < MI; ++i) sa_[i] = ld16(ak + (size_t)ao[i]);
   };
   auto store = [&]() {
 #pragma unroll
@@ -338,16 +342,35 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
       *reinterpret_cast<uint4 *>(lds + a_put + 32 * BG_KS * i) = sa_[i];
   };
   i32x4_t acc[MI][4] = {};
-  auto multiply = [&](int h) {   // K 64 h .. 64 h + 63 of the step: chunks 4 h + lg
-    uint4 wv[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f)
+  // One step.  Row fragment q (half h = q / MI of the step, chunks 4 h + lg)
+  // is read two fragments before it is multiplied, the second half's channel
+  // fragments as the first half's are used up; the scheduler keeps that order
+  // (left alone, it reads each fragment right before its use and waits).
+  auto multiply = [&]() {
+    uint4 wv[4], av[3];
+    auto read_w = [&](int h, int f) {
       wv[f] = *reinterpret_cast<const uint4 *>(lds + (w_get ^ (64 * h)) + BG_KS * gt_col(f, 0));
+    };
+    auto read_a = [&](int q) {
+      av[q % 3] = *reinterpret_cast<const uint4 *>(
+          lds + (a_get ^ (64 * (q / MI))) + 32 * BG_KS * (q % MI));
+    };
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const uint4 av = *reinterpret_cast<const uint4 *>(lds + (a_get ^ (64 * h)) + 32 * BG_KS * i);
+    for (int f = 0; f < 4; ++f) read_w(0, f);
+    read_a(0);
+    read_a(1);
 #pragma unroll
-      for (int f = 0; f < 4; ++f) acc[i][f] = mfma_i8(wv[f], av, acc[i][f]);
+    for (int q = 0; q < 2 * MI; ++q) {
+      if (q + 2 < 2 * MI) read_a(q + 2);
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        acc[q % MI][f] = mfma_i8(wv[f], av[q % 3], acc[q % MI][f]);
+        if (q == MI - 1) {
+          __builtin_amdgcn_sched_barrier(0);
+          read_w(1, f);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
   load(0);
@@ -357,8 +380,7 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
     load(j + 1);
     __builtin_amdgcn_s_waitcnt(kWaitLds);
     block_barrier();
-    multiply(0);
-    multiply(1);
+    multiply();
     block_barrier();
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -435,7 +457,8 @@ template <typename T> static void launch_big(const LinearI8Args &A, hipStream_t 
 
 template <typename T> static void launch_linear(const LinearI8Args &A, hipStream_t st) {
   const int avg = A.M / A.E;
-  if (avg > 64) launch_big<T>(A, st);
+  const bool near = (uint64_t)A.N * A.ldw < (1ull << 32) && (uint64_t)A.a_rows * A.lda < (1ull << 32);
+  if (avg > 64 && near) launch_big<T>(A, st);
   else if (avg <= 8) launch_short<T, 1, 4>(A, st);
   else if (avg <= 24) launch_short<T, 2, 4>(A, st);
   else launch_short<T, 4, 8>(A, st);

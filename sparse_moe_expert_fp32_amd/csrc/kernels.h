@@ -313,7 +313,7 @@ void launch_router_bwd(bool bf16, const void *x, const float *w, const uint8_t *
 
 // ---- int8 rows and products (quant_i8.hip, linear_i8.hip)
 struct QuantArgs {
-  int M, K, E;
+  int p0, M, K, E;                           // rows p0 .. p0 + M - 1
   const void *x, *u; int64_t ldx, ldu;       // u: SwiGLU of x and u, or null
   const float *col_scale;                    // [E][K] or null
   const int32_t *offsets;                    // [E + 1] or null (every row of expert 0)

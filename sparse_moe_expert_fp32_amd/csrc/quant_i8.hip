@@ -74,8 +74,8 @@ template <typename T, int NT, int NH, bool VEC>
 __global__ __launch_bounds__(256) void quant_i8_kernel(QuantArgs A) {
   constexpr int RB = 256 / NT;              // rows per block
   __shared__ uint32_t red[4];
-  const int tid = threadIdx.x % NT, p = blockIdx.x * RB + threadIdx.x / NT;
-  if (p >= A.M || (A.offsets && p >= A.offsets[A.E])) return;   // (NT = 256: the whole block)
+  const int tid = threadIdx.x % NT, p = A.p0 + blockIdx.x * RB + threadIdx.x / NT;
+  if (p >= A.p0 + A.M || (A.offsets && p >= A.offsets[A.E])) return;   // (NT = 256: the whole block)
   const T *x = (const T *)A.x + (size_t)p * A.ldx;
   const T *u = A.u ? (const T *)A.u + (size_t)p * A.ldu : nullptr;
   const float *cs = nullptr;
@@ -164,7 +164,17 @@ template <typename T, bool VEC> static void quant_launch(const QuantArgs &A, hip
 #undef MOE_Q
 }
 
-void launch_quant_i8(bool bf16, const QuantArgs &A, hipStream_t st) {
+void launch_quant_i8(bool bf16, const QuantArgs &all, hipStream_t st) {
+  constexpr int kRows = 1 << 22;   // per launch: a grid's threads are counted in 32 bits
+  QuantArgs A = all;
+  if (all.M > kRows) {
+    for (int p = 0; p < all.M; p += kRows) {
+      A.p0 = all.p0 + p;
+      A.M = std::min(kRows, all.M - p);
+      launch_quant_i8(bf16, A, st);
+    }
+    return;
+  }
   const int ab = bf16 ? 2 : 4;
   const bool vec = A.K % 8 == 0 &&
                    (((uintptr_t)A.x | (uintptr_t)(A.ldx * ab)) & 15) == 0 &&

@@ -15,6 +15,7 @@
 
 #include "common.h"
 #include "kernels.h"
+#include "mfma.h"
 
 namespace moe {
 
@@ -125,52 +126,263 @@ void launch_gate_bwd(bool bf16, const void *dy, const void *e_out, const int32_t
 #undef MOE_GB
 }
 
-// C[m][n] = add[m][n] + sum_k A(m, k) B(k, n) in float32, 64 x 64 tile per
-// 256-thread block, 16-deep LDS stages.  A(m, k) = a[m * am + k * ak], B(k, n)
-// = b[k * bk + n * bn].  von: row mask over k (VK) or m of the operand A and,
-// for VK, of B.
-template <typename TA, typename TC, bool VK>
-__global__ __launch_bounds__(256) void gemm_f32_kernel(
-    const TA *__restrict__ a, size_t am, size_t ak, const float *__restrict__ b, size_t bk,
-    size_t bn, int M, int N, int K, const uint8_t *__restrict__ von, const TC *add,
-    TC *out) {
-  __shared__ float As[16][65], Bs[16][65];
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int m0 = blockIdx.x * 64, n0 = blockIdx.y * 64;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += 16) {
-    for (int i = tid; i < 1024; i += 256) {
-      // consecutive threads along the operand's contiguous direction
-      const int ka = ak == 1 ? i & 15 : i >> 6, ma = ak == 1 ? i >> 4 : i & 63;
-      const int kb = bk == 1 ? i & 15 : i >> 6, nb = bk == 1 ? i >> 4 : i & 63;
-      const bool oa = k0 + ka < K && m0 + ma < M && (!von || von[VK ? k0 + ka : m0 + ma]);
-      const bool ob = k0 + kb < K && n0 + nb < N && (!VK || !von || von[k0 + kb]);
-      As[ka][ma] = oa ? Elem<TA>::ld(a, (size_t)(m0 + ma) * am + (size_t)(k0 + ka) * ak) : 0.f;
-      Bs[kb][nb] = ob ? b[(size_t)(k0 + kb) * bk + (size_t)(n0 + nb) * bn] : 0.f;
-    }
-    __syncthreads();
+// ---- the two products in float32 accuracy on the bf16 matrix cores.
+//
+// A float32 value is the sum of three bf16 values exactly (8 + 8 + 8 bits of
+// its significand, cut off, not rounded), a bf16 value is one.  So
+//   C[m][n] = sum_k A(m, k) B(n, k)
+// is the sum of the products of such planes; the planes i, j with i + j < 3
+// are kept for float32 results (what is left out is below 2^-24 of a product),
+// and i + j < 2 for results that are rounded to bf16 (two planes, the second
+// one rounded: 2^-16).  Three matrix instructions of 16 clocks in the place of
+// the eight of 32 that float32 operands take (v_mfma_f32_16x16x4_f32).
+//
+// 128 x BN tile per block of four waves (2 x 2), steps of 32 along k through
+// two LDS slots; a step's values are loaded while the one before it is
+// multiplied and split into planes on their way into LDS.  An operand lies
+// with k adjacent (KADJ: rows of k) or with k as its row index (a thread then
+// takes eight rows of one column; neighbouring threads neighbouring columns).
+constexpr int RB_BM = 128, RB_KS = 32;
+
+template <int P> struct Planes { uint4 v[P]; };
+
+// 8 values -> planes
+template <int P> DEV Planes<P> split8(const float *f) {
+  Planes<P> S;
+  float r[8];
 #pragma unroll
-    for (int kk = 0; kk < 16; ++kk) {
-      float av[4], bv[4];
+  for (int i = 0; i < 8; ++i) r[i] = f[i];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) { av[i] = As[kk][ty * 4 + i]; bv[i] = Bs[kk][tx + 16 * i]; }
+  for (int p = 0; p < P; ++p) {
+    uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty * 4 + i, n = n0 + tx + 16 * j;
-      if (m < M && n < N) {
-        const size_t o = (size_t)m * N + n;
-        Elem<TC>::st(out, o, acc[i][j] + (add ? Elem<TC>::ld(add, o) : 0.f));
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = __float_as_uint(r[2 * i]), hi = __float_as_uint(r[2 * i + 1]);
+      if (p == 1 && P == 2) {
+        o[i] = cvt_pk_bf16(r[2 * i], r[2 * i + 1]);
+      } else {
+        o[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);   // the upper halves
+        if (p + 1 < P) {
+          r[2 * i] -= __uint_as_float(lo & 0xFFFF0000u);
+          r[2 * i + 1] -= __uint_as_float(hi & 0xFFFF0000u);
+        }
       }
     }
+    S.v[p] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  return S;
+}
+
+// One operand of a block: R rows (m or n) from r0 on.  Thread items: row and
+// 8-wide chunk of k; IT items per thread.
+template <typename T, int R, bool KADJ> struct Operand {
+  static constexpr int IT = R * 4 / 256;
+  const T *p;           // [rows][ld] (KADJ) or [k][ld]
+  size_t ld;
+  int rows, r0;
+  bool vec;             // KADJ: 16-byte accesses
+  const uint8_t *von;   // mask over k (not KADJ) or over the rows (KADJ), or null
+  float v[IT][8];
+
+  DEV int row(int i) const { return KADJ ? (threadIdx.x >> 2) + 64 * i : (threadIdx.x + 256 * i) % R; }
+  DEV int chunk(int i) const { return KADJ ? threadIdx.x & 3 : (threadIdx.x + 256 * i) / R; }
+  DEV void load(int k0, int k1) {   // k in [k0, k0 + 32), those at k1 and behind are 0
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int r = r0 + row(i), k = k0 + 8 * chunk(i);
+      if constexpr (KADJ) {
+        const bool on = r < rows && (!von || von[r]);
+        const T *q = p + (size_t)min(r, rows - 1) * ld;
+        if (vec && k + 8 <= k1) {
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+          if (on) {
+            a = *reinterpret_cast<const float4 *>(q + k);
+            b = *reinterpret_cast<const float4 *>(q + k + 4);
+          }
+          v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
+          v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
+        } else {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) v[i][u] = on && k + u < k1 ? Elem<T>::ld(q, k + u) : 0.f;
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const bool on = r < rows && k + u < k1 && (!von || von[k + u]);
+          v[i][u] = on ? Elem<T>::ld(p, (size_t)(k + u) * ld + r) : 0.f;
+        }
+      }
+    }
+  }
+  // planes of 64-byte rows; chunk c of row r at place c ^ (r >> 2) & 3, so that
+  // 16 lanes reading one chunk of 16 rows touch every bank once
+  template <int P> DEV void store(uint8_t *lds) const {
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const Planes<P> S = split8<P>(v[i]);
+#pragma unroll
+      for (int q = 0; q < P; ++q)
+        *reinterpret_cast<uint4 *>(lds + q * R * 64 + row(i) * 64 +
+                                   ((chunk(i) ^ (row(i) >> 2)) & 3) * 16) = S.v[q];
+    }
+  }
+};
+
+struct RouterGemmArgs {
+  const void *a; size_t lda; const float *b; size_t ldb;
+  int M, N, K, klen;                     // klen: k per blockIdx.y
+  const uint8_t *von;
+  const void *add;                       // ADD: [M][N] or null
+  void *out;                             // [M][N], or partials [z][M][N] f32
+  float *colsum;                         // [z][N]: sums of B over k (blocks of the first rows), or null
+};
+
+template <typename TA, typename TC, int BN, bool KADJ, int PA, int PB>
+__global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
+  constexpr int PM = PA > PB ? PA : PB, NF = BN / 32;
+  constexpr int SLOT = (PA * RB_BM + PB * BN) * 64;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * SLOT];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, lr = lane & 15, lg = lane >> 4;
+  const int wm = w & 1, wn = w >> 1;
+  const int nx = (G.N + BN - 1) / BN, by = blockIdx.x / nx;   // column tiles of a row tile in turn
+  const int m0 = by * RB_BM, n0 = (blockIdx.x - by * nx) * BN;
+  const int kb = blockIdx.y * G.klen, ke = min(G.K, kb + G.klen);
+  Operand<TA, RB_BM, KADJ> A{(const TA *)G.a, G.lda, G.M, m0, false, G.von};
+  Operand<float, BN, KADJ> B{G.b, G.ldb, G.N, n0, false, KADJ ? nullptr : G.von};
+  if constexpr (KADJ) {
+    A.vec = ((((uintptr_t)G.a) | (G.lda * sizeof(TA))) & 15) == 0;
+    B.vec = ((((uintptr_t)G.b) | (G.ldb * 4)) & 15) == 0;
+  }
+  f32x4_t acc[4][NF] = {};
+  float cs[Operand<float, BN, KADJ>::IT] = {};
+  const int get = lr * 64 + ((lg ^ (lr >> 2)) & 3) * 16;
+  A.load(kb, ke);
+  B.load(kb, ke);
+  for (int k = kb, g = 0; k < ke; k += RB_KS, g ^= 1) {
+    uint8_t *slot = lds + g * SLOT, *sb = slot + PA * RB_BM * 64;
+    A.template store<PA>(slot);
+    B.template store<PB>(sb);
+    if constexpr (!KADJ) {
+      if (G.colsum && by == 0) {
+#pragma unroll
+        for (int i = 0; i < Operand<float, BN, KADJ>::IT; ++i)
+#pragma unroll
+          for (int u = 0; u < 8; ++u) cs[i] += B.v[i][u];
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (k + RB_KS < ke) {
+      A.load(k + RB_KS, ke);
+      B.load(k + RB_KS, ke);
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // (LDS only: the loads stay in flight)
+    block_barrier();
+    uint4 av[PA][4];
+#pragma unroll
+    for (int p = 0; p < PA; ++p)
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        av[p][m] = *reinterpret_cast<const uint4 *>(slot + (p * RB_BM + 64 * wm + 16 * m) * 64 + get);
+#pragma unroll
+    for (int p = 0; p < PB; ++p)
+#pragma unroll
+      for (int n = 0; n < NF; ++n) {
+        const uint4 bv = *reinterpret_cast<const uint4 *>(sb + (p * BN + (BN / 2) * wn + 16 * n) * 64 + get);
+#pragma unroll
+        for (int q = 0; q < PA; ++q)
+          if (p + q < PM) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) acc[m][n] = mfma32(bv, av[q][m], acc[m][n]);
+          }
+      }
+  }
+  // a lane has columns n0 + .. + 4 lg + 0..3 of row lr of each fragment
+  TC *out = (TC *)G.out + (size_t)blockIdx.y * G.M * G.N;
+  const TC *add = (const TC *)G.add;
+  const bool vec = G.N % 4 == 0 && (((uintptr_t)out | (uintptr_t)add) & (4 * sizeof(TC) - 1)) == 0;
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const int r = m0 + 64 * wm + 16 * m + lr;
+    if (r >= G.M) continue;
+#pragma unroll
+    for (int n = 0; n < NF; ++n) {
+      const int c = n0 + (BN / 2) * wn + 16 * n + 4 * lg;
+      const size_t o = (size_t)r * G.N + c;
+      if (c >= G.N) continue;
+      float v[4] = {acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]};
+      if (vec) {   // (N is a multiple of 4: the four columns are there)
+        if constexpr (sizeof(TC) == 2) {
+          if (add) {
+            const uint2 d = *reinterpret_cast<const uint2 *>(add + o);
+            v[0] += __uint_as_float(d.x << 16); v[1] += __uint_as_float(d.x & 0xFFFF0000u);
+            v[2] += __uint_as_float(d.y << 16); v[3] += __uint_as_float(d.y & 0xFFFF0000u);
+          }
+          *reinterpret_cast<uint2 *>(out + o) =
+              make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
+        } else {
+          if (add) {
+            const float4 d = *reinterpret_cast<const float4 *>(add + o);
+            v[0] += d.x; v[1] += d.y; v[2] += d.z; v[3] += d.w;
+          }
+          *reinterpret_cast<float4 *>(out + o) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c + i < G.N) {
+            const float s = v[i] + (add ? Elem<TC>::ld(add, o + i) : 0.f);
+            if constexpr (sizeof(TC) == 2) out[o + i] = (uint16_t)cvt_pk_bf16(s, s);
+            else out[o + i] = s;
+          }
+      }
+    }
+  }
+  if constexpr (!KADJ) {
+    if (G.colsum && by == 0) {   // the threads of a column, in order
+      float *red = reinterpret_cast<float *>(lds);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < Operand<float, BN, KADJ>::IT; ++i) red[B.chunk(i) * BN + B.row(i)] = cs[i];
+      __syncthreads();
+      if (tid < BN && n0 + tid < G.N) {
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s += red[q * BN + tid];
+        G.colsum[(size_t)blockIdx.y * G.N + n0 + tid] = s;
+      }
+    }
+  }
+}
+
+// out[i] = sum_z part[z][i] (z ascending) for the weight gradient (n values)
+// and the bias gradient (E values; null without one)
+__global__ __launch_bounds__(256) void router_sum_kernel(const float *__restrict__ part,
+                                                         const float *__restrict__ cpart, int z,
+                                                         size_t n, int E, float *__restrict__ out,
+                                                         float *__restrict__ db) {
+  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i < n) {
+    if (n % 4 == 0 && ((uintptr_t)out & 15) == 0) {
+      float4 s = *reinterpret_cast<const float4 *>(part + i);
+      for (int q = 1; q < z; ++q) {
+        const float4 v = *reinterpret_cast<const float4 *>(part + q * n + i);
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      }
+      *reinterpret_cast<float4 *>(out + i) = s;
+    } else {
+      for (size_t j = i; j < n && j < i + 4; ++j) {
+        float s = part[j];
+        for (int q = 1; q < z; ++q) s += part[q * n + j];
+        out[j] = s;
+      }
+    }
+  }
+  const int e = blockIdx.x * 256 + threadIdx.x;
+  if (db && e < E) {
+    float s = cpart[e];
+    for (int q = 1; q < z; ++q) s += cpart[(size_t)q * E + e];
+    db[e] = s;
+  }
 }
 
 __global__ __launch_bounds__(1024) void colsum_kernel(const float *__restrict__ a,
@@ -190,34 +402,60 @@ __global__ __launch_bounds__(1024) void colsum_kernel(const float *__restrict__ 
   }
 }
 
+// The weight gradient's sum over tokens is split so that its tiles fill the
+// chip (two blocks per CU), each part at least 256 tokens.
+struct RouterSplit { int bn, z, klen; };
+static RouterSplit router_split(int T, int d, int E) {
+  RouterSplit S;
+  S.bn = E <= 64 ? 64 : 128;
+  const int tiles = ceil_div_h(d, RB_BM) * ceil_div_h(E, S.bn);
+  const int z = std::max(1, std::min(512 / tiles, ceil_div_h(T, 256)));
+  S.klen = ceil_div_h(ceil_div_h(T, z), RB_KS) * RB_KS;
+  S.z = ceil_div_h(T, S.klen);
+  return S;
+}
+
 size_t router_bwd_ws_bytes(int T, int d, int E) {
-  (void)T; (void)d; (void)E;
-  return 0;
+  const RouterSplit S = router_split(T, d, E);
+  return S.z > 1 ? (size_t)S.z * ((size_t)d * E + E) * 4 + 16 : 0;
+}
+
+template <typename TX> static void router_bwd(const void *x, const float *w, const uint8_t *valid,
+                                              const float *dl, const void *dx_in, int T, int d,
+                                              int E, void *dx, float *dw, float *db, void *ws,
+                                              hipStream_t st) {
+  constexpr bool f32 = sizeof(TX) == 4;
+  if (dx) {
+    RouterGemmArgs G{dl, (size_t)E, w, (size_t)E, T, d, E, ceil_div_h(E, RB_KS) * RB_KS, valid,
+                     dx_in, dx, nullptr};
+    const unsigned grid = (unsigned)ceil_div_h(d, 128) * ceil_div_h(T, RB_BM);
+    if constexpr (f32) router_gemm_kernel<float, float, 128, true, 3, 3><<<grid, 256, 0, st>>>(G);
+    else router_gemm_kernel<float, bf16_t, 128, true, 2, 2><<<grid, 256, 0, st>>>(G);
+  }
+  if (dw) {
+    const RouterSplit S = router_split(T, d, E);
+    const size_t n = (size_t)d * E;
+    float *part = S.z > 1 ? (float *)ws : dw;
+    float *cpart = S.z > 1 ? (float *)ws + ((S.z * n + 3) & ~size_t(3)) : db;
+    RouterGemmArgs G{x, (size_t)d, dl, (size_t)E, d, E, T, S.klen, valid, nullptr, part,
+                     db ? cpart : nullptr};
+    const dim3 grid(ceil_div_h(E, S.bn) * ceil_div_h(d, RB_BM), S.z);
+    constexpr int PX = f32 ? 3 : 1;
+    if (S.bn == 64) router_gemm_kernel<TX, float, 64, false, PX, 3><<<grid, 256, 0, st>>>(G);
+    else router_gemm_kernel<TX, float, 128, false, PX, 3><<<grid, 256, 0, st>>>(G);
+    if (S.z > 1)
+      router_sum_kernel<<<(unsigned)((n + 1023) / 1024 + (E + 255) / 256), 256, 0, st>>>(
+          part, cpart, S.z, n, E, dw, db);
+  } else if (db) {
+    colsum_kernel<<<(E + 63) / 64, 1024, 0, st>>>(dl, valid, T, E, db);
+  }
 }
 
 void launch_router_bwd(bool bf16, const void *x, const float *w, const uint8_t *valid,
                        const float *dl, const void *dx_in, int T, int d, int E, void *dx,
                        float *dw, float *db, void *ws, hipStream_t st) {
-  (void)ws;
-  if (dx) {
-    dim3 grid((T + 63) / 64, (d + 63) / 64);
-    if (bf16)
-      gemm_f32_kernel<float, bf16_t, false><<<grid, 256, 0, st>>>(
-          dl, (size_t)E, 1, w, 1, (size_t)E, T, d, E, valid, (const bf16_t *)dx_in, (bf16_t *)dx);
-    else
-      gemm_f32_kernel<float, float, false><<<grid, 256, 0, st>>>(
-          dl, (size_t)E, 1, w, 1, (size_t)E, T, d, E, valid, (const float *)dx_in, (float *)dx);
-  }
-  if (dw) {
-    dim3 grid((d + 63) / 64, (E + 63) / 64);
-    if (bf16)
-      gemm_f32_kernel<bf16_t, float, true><<<grid, 256, 0, st>>>(
-          (const bf16_t *)x, 1, (size_t)d, dl, (size_t)E, 1, d, E, T, valid, nullptr, dw);
-    else
-      gemm_f32_kernel<float, float, true><<<grid, 256, 0, st>>>(
-          (const float *)x, 1, (size_t)d, dl, (size_t)E, 1, d, E, T, valid, nullptr, dw);
-  }
-  if (db) colsum_kernel<<<(E + 63) / 64, 1024, 0, st>>>(dl, valid, T, E, db);
+  if (bf16) router_bwd<bf16_t>(x, w, valid, dl, dx_in, T, d, E, dx, dw, db, ws, st);
+  else router_bwd<float>(x, w, valid, dl, dx_in, T, d, E, dx, dw, db, ws, st);
 }
 
 }  // namespace moe

@@ -174,52 +174,92 @@ template <int P> DEV Planes<P> split8(const float *f) {
 }
 
 // One operand of a block: R rows (m or n) from r0 on.  Thread items: row and
-// 8-wide chunk of k; IT items per thread.
+// 8-wide chunk of k; IT items per thread.  load() only asks memory (addresses
+// held inside the operand, no condition on a value); what lies outside or is
+// masked becomes 0 in store().
 template <typename T, int R, bool KADJ> struct Operand {
   static constexpr int IT = R * 4 / 256;
   const T *p;           // [rows][ld] (KADJ) or [k][ld]
   size_t ld;
   int rows, r0;
-  bool vec;             // KADJ: 16-byte accesses
+  bool vec;             // KADJ: 16-byte accesses (ld and k1 multiples of 4)
   const uint8_t *von;   // mask over k (not KADJ) or over the rows (KADJ), or null
-  float v[IT][8];
+  int k0, k1;           // the step on its way: [k0, k0 + 32), those at k1 and behind are 0
+  T v[IT][8];
+  uint8_t on[IT][8];    // masks of the step (not KADJ), or of the rows ([.][0])
+  const T *at[IT];      // KADJ: the rows
 
   DEV int row(int i) const { return KADJ ? (threadIdx.x >> 2) + 64 * i : (threadIdx.x + 256 * i) % R; }
-  DEV int chunk(int i) const { return KADJ ? threadIdx.x & 3 : (threadIdx.x + 256 * i) / R; }
-  DEV void load(int k0, int k1) {   // k in [k0, k0 + 32), those at k1 and behind are 0
+  DEV int chunk(int i) const {   // not KADJ: the same in a whole wave
+    return KADJ ? threadIdx.x & 3 : __builtin_amdgcn_readfirstlane((threadIdx.x + 256 * i) / R);
+  }
+  DEV void init() {
+    if constexpr (KADJ) {
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int r = r0 + row(i), k = k0 + 8 * chunk(i);
-      if constexpr (KADJ) {
-        const bool on = r < rows && (!von || von[r]);
-        const T *q = p + (size_t)min(r, rows - 1) * ld;
-        if (vec && k + 8 <= k1) {
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-          if (on) {
-            a = *reinterpret_cast<const float4 *>(q + k);
-            b = *reinterpret_cast<const float4 *>(q + k + 4);
-          }
-          v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
-          v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
-        } else {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) v[i][u] = on && k + u < k1 ? Elem<T>::ld(q, k + u) : 0.f;
-        }
-      } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const bool on = r < rows && k + u < k1 && (!von || von[k + u]);
-          v[i][u] = on ? Elem<T>::ld(p, (size_t)(k + u) * ld + r) : 0.f;
-        }
+      for (int i = 0; i < IT; ++i) {
+        const int r = min(r0 + row(i), rows - 1);
+        at[i] = p + (size_t)r * ld;
+        on[i][0] = r0 + row(i) < rows && (!von || von[r]);
       }
     }
   }
-  // planes of 64-byte rows; chunk c of row r at place c ^ (r >> 2) & 3, so that
-  // 16 lanes reading one chunk of 16 rows touch every bank once
-  template <int P> DEV void store(uint8_t *lds) const {
+  DEV void load(int k0_, int k1_) {
+    k0 = k0_;
+    k1 = k1_;
+    if constexpr (!KADJ) {
+      if (von) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+#pragma unroll
+          for (int u = 0; u < 8; ++u) on[i][u] = von[min(k0 + 8 * chunk(i) + u, k1 - 1)];
+      }
+    }
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const Planes<P> S = split8<P>(v[i]);
+      const int k = k0 + 8 * chunk(i);
+      if constexpr (KADJ) {
+        if (vec) {
+          if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float4 a = *reinterpret_cast<const float4 *>(at[i] + min(k + 4 * h, k1 - 4));
+              v[i][4 * h] = a.x; v[i][4 * h + 1] = a.y; v[i][4 * h + 2] = a.z; v[i][4 * h + 3] = a.w;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) v[i][u] = at[i][min(k + u, k1 - 1)];
+        }
+      } else {
+        const uint32_t r = min(r0 + row(i), rows - 1);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[i][u] = (p + (size_t)min(k + u, k1 - 1) * ld)[r];
+      }
+    }
+  }
+  // value u of item i, as float32 (0 outside)
+  DEV float value(int i, int u) const {
+    const int k = k0 + 8 * chunk(i) + u;
+    const float f = Elem<T>::ld(&v[i][u], 0);
+    bool ok = k < k1;
+    if constexpr (KADJ) ok = ok && on[i][0];
+    else ok = ok && r0 + row(i) < rows && (!von || on[i][u]);
+    return ok ? f : 0.f;
+  }
+  // planes of 64-byte rows; chunk c of row r at place c ^ (r >> 2) & 3, so that
+  // 16 lanes reading one chunk of 16 rows touch every bank once.  sum: the
+  // items' values added up
+  template <int P> DEV void store(uint8_t *lds, float *sum = nullptr) const {
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      float f[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) f[u] = value(i, u);
+      if (sum) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) sum[i] += f[u];
+      }
+      const Planes<P> S = split8<P>(f);
 #pragma unroll
       for (int q = 0; q < P; ++q)
         *reinterpret_cast<uint4 *>(lds + q * R * 64 + row(i) * 64 +
@@ -247,12 +287,14 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
   const int nx = (G.N + BN - 1) / BN, by = blockIdx.x / nx;   // column tiles of a row tile in turn
   const int m0 = by * RB_BM, n0 = (blockIdx.x - by * nx) * BN;
   const int kb = blockIdx.y * G.klen, ke = min(G.K, kb + G.klen);
-  Operand<TA, RB_BM, KADJ> A{(const TA *)G.a, G.lda, G.M, m0, false, G.von};
-  Operand<float, BN, KADJ> B{G.b, G.ldb, G.N, n0, false, KADJ ? nullptr : G.von};
-  if constexpr (KADJ) {
-    A.vec = ((((uintptr_t)G.a) | (G.lda * sizeof(TA))) & 15) == 0;
-    B.vec = ((((uintptr_t)G.b) | (G.ldb * 4)) & 15) == 0;
-  }
+  Operand<TA, RB_BM, KADJ> A;
+  A.p = (const TA *)G.a; A.ld = G.lda; A.rows = G.M; A.r0 = m0; A.von = G.von;
+  Operand<float, BN, KADJ> B;
+  B.p = G.b; B.ld = G.ldb; B.rows = G.N; B.r0 = n0; B.von = KADJ ? nullptr : G.von;
+  A.vec = ((((uintptr_t)G.a) | (G.lda * sizeof(TA))) & 15) == 0 && ke % 4 == 0;
+  B.vec = ((((uintptr_t)G.b) | (G.ldb * 4)) & 15) == 0 && ke % 4 == 0;
+  A.init();
+  B.init();
   f32x4_t acc[4][NF] = {};
   float cs[Operand<float, BN, KADJ>::IT] = {};
   const int get = lr * 64 + ((lg ^ (lr >> 2)) & 3) * 16;
@@ -261,15 +303,7 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
   for (int k = kb, g = 0; k < ke; k += RB_KS, g ^= 1) {
     uint8_t *slot = lds + g * SLOT, *sb = slot + PA * RB_BM * 64;
     A.template store<PA>(slot);
-    B.template store<PB>(sb);
-    if constexpr (!KADJ) {
-      if (G.colsum && by == 0) {
-#pragma unroll
-        for (int i = 0; i < Operand<float, BN, KADJ>::IT; ++i)
-#pragma unroll
-          for (int u = 0; u < 8; ++u) cs[i] += B.v[i][u];
-      }
-    }
+    B.template store<PB>(sb, KADJ ? nullptr : cs);
     __builtin_amdgcn_sched_barrier(0);
     if (k + RB_KS < ke) {
       A.load(k + RB_KS, ke);

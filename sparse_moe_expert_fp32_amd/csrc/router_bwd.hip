@@ -173,25 +173,29 @@ template <int P> DEV Planes<P> split8(const float *f) {
   return S;
 }
 
-// One operand of a block: R rows (m or n) from r0 on.  Thread items: row and
-// 8-wide chunk of k; IT items per thread.  load() only asks memory (addresses
-// held inside the operand, no condition on a value); what lies outside or is
-// masked becomes 0 in store().
-template <typename T, int R, bool KADJ> struct Operand {
-  static constexpr int IT = R * 4 / 256;
+// One operand of a block: R rows (m or n) from r0 on.  Thread items: a row (a
+// pair of rows of bf16 with k as the row index) and an 8-wide chunk of k; IT
+// items per thread.  load() only asks memory (addresses held inside the
+// operand, no condition on a value); what lies outside or is masked becomes 0
+// in store(), which asks only where a step is not whole.  VEC: k adjacent,
+// rows at multiples of 16 bytes, k1 a multiple of 4.
+template <typename T, int R, bool KADJ, bool VEC> struct Operand {
+  static constexpr bool PAIR = !KADJ && sizeof(T) == 2;
+  static constexpr int IT = R * 4 / 256 / (PAIR ? 2 : 1), RI = R / (PAIR ? 2 : 1);
   const T *p;           // [rows][ld] (KADJ) or [k][ld]
   size_t ld;
   int rows, r0;
-  bool vec;             // KADJ: 16-byte accesses (ld and k1 multiples of 4)
   const uint8_t *von;   // mask over k (not KADJ) or over the rows (KADJ), or null
   int k0, k1;           // the step on its way: [k0, k0 + 32), those at k1 and behind are 0
-  T v[IT][8];
+  float v[IT][8];       // (PAIR: the bits of two bf16 columns)
   uint8_t on[IT][8];    // masks of the step (not KADJ), or of the rows ([.][0])
   const T *at[IT];      // KADJ: the rows
 
-  DEV int row(int i) const { return KADJ ? (threadIdx.x >> 2) + 64 * i : (threadIdx.x + 256 * i) % R; }
+  DEV int row(int i) const {
+    return KADJ ? (threadIdx.x >> 2) + 64 * i : (threadIdx.x + 256 * i) % RI * (PAIR ? 2 : 1);
+  }
   DEV int chunk(int i) const {   // not KADJ: the same in a whole wave
-    return KADJ ? threadIdx.x & 3 : __builtin_amdgcn_readfirstlane((threadIdx.x + 256 * i) / R);
+    return KADJ ? threadIdx.x & 3 : __builtin_amdgcn_readfirstlane((threadIdx.x + 256 * i) / RI);
   }
   DEV void init() {
     if constexpr (KADJ) {
@@ -217,53 +221,69 @@ template <typename T, int R, bool KADJ> struct Operand {
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       const int k = k0 + 8 * chunk(i);
-      if constexpr (KADJ) {
-        if (vec) {
-          if constexpr (sizeof(T) == 4) {
+      if constexpr (KADJ && VEC) {
+        static_assert(sizeof(T) == 4, "float32 rows");
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float4 a = *reinterpret_cast<const float4 *>(at[i] + min(k + 4 * h, k1 - 4));
-              v[i][4 * h] = a.x; v[i][4 * h + 1] = a.y; v[i][4 * h + 2] = a.z; v[i][4 * h + 3] = a.w;
-            }
-          }
-        } else {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) v[i][u] = at[i][min(k + u, k1 - 1)];
+        for (int h = 0; h < 2; ++h) {
+          const float4 a = *reinterpret_cast<const float4 *>(at[i] + min(k + 4 * h, k1 - 4));
+          v[i][4 * h] = a.x; v[i][4 * h + 1] = a.y; v[i][4 * h + 2] = a.z; v[i][4 * h + 3] = a.w;
         }
-      } else {
-        const uint32_t r = min(r0 + row(i), rows - 1);
+      } else if constexpr (KADJ) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[i][u] = (p + (size_t)min(k + u, k1 - 1) * ld)[r];
+        for (int u = 0; u < 8; ++u) v[i][u] = at[i][min(k + u, k1 - 1)];
+      } else {
+        // (PAIR: rows and ld are even, the pair is one aligned word)
+        const uint32_t r = min(r0 + row(i), rows - (PAIR ? 2 : 1));
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          v[i][u] = *reinterpret_cast<const float *>((p + (size_t)min(k + u, k1 - 1) * ld) + r);
       }
     }
   }
-  // value u of item i, as float32 (0 outside)
-  DEV float value(int i, int u) const {
-    const int k = k0 + 8 * chunk(i) + u;
-    const float f = Elem<T>::ld(&v[i][u], 0);
-    bool ok = k < k1;
+  // whether nothing of the step is outside or masked
+  DEV bool whole() const { return k0 + RB_KS <= k1 && r0 + R <= rows && !von; }
+  DEV bool inside(int i, int u) const {
+    bool ok = k0 + 8 * chunk(i) + u < k1;
     if constexpr (KADJ) ok = ok && on[i][0];
     else ok = ok && r0 + row(i) < rows && (!von || on[i][u]);
-    return ok ? f : 0.f;
+    return ok;
+  }
+  DEV static uint8_t *place(uint8_t *lds, int r, int c) {
+    return lds + r * 64 + ((c ^ (r >> 2)) & 3) * 16;
   }
   // planes of 64-byte rows; chunk c of row r at place c ^ (r >> 2) & 3, so that
   // 16 lanes reading one chunk of 16 rows touch every bank once.  sum: the
   // items' values added up
-  template <int P> DEV void store(uint8_t *lds, float *sum = nullptr) const {
+  template <int P> DEV void store(uint8_t *lds, float *sum = nullptr) {
+    if (!whole()) {
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[i][u] = inside(i, u) ? v[i][u] : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      float f[8];
+      if constexpr (PAIR) {
+        static_assert(P == 1, "a bf16 value is one plane");
+        uint32_t lo[4], hi[4];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) f[u] = value(i, u);
-      if (sum) {
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x = __float_as_uint(v[i][2 * j]), y = __float_as_uint(v[i][2 * j + 1]);
+          lo[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+          hi[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+        }
+        *reinterpret_cast<uint4 *>(place(lds, row(i), chunk(i))) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4 *>(place(lds, row(i) + 1, chunk(i))) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      } else {
+        if (sum) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) sum[i] += f[u];
+          for (int u = 0; u < 8; ++u) sum[i] += v[i][u];
+        }
+        const Planes<P> S = split8<P>(v[i]);
+#pragma unroll
+        for (int q = 0; q < P; ++q)
+          *reinterpret_cast<uint4 *>(place(lds + q * R * 64, row(i), chunk(i))) = S.v[q];
       }
-      const Planes<P> S = split8<P>(f);
-#pragma unroll
-      for (int q = 0; q < P; ++q)
-        *reinterpret_cast<uint4 *>(lds + q * R * 64 + row(i) * 64 +
-                                   ((chunk(i) ^ (row(i) >> 2)) & 3) * 16) = S.v[q];
     }
   }
 };
@@ -277,7 +297,7 @@ struct RouterGemmArgs {
   float *colsum;                         // [z][N]: sums of B over k (blocks of the first rows), or null
 };
 
-template <typename TA, typename TC, int BN, bool KADJ, int PA, int PB>
+template <typename TA, typename TC, int BN, bool KADJ, bool VEC, int PA, int PB>
 __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
   constexpr int PM = PA > PB ? PA : PB, NF = BN / 32;
   constexpr int SLOT = (PA * RB_BM + PB * BN) * 64;
@@ -287,16 +307,14 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
   const int nx = (G.N + BN - 1) / BN, by = blockIdx.x / nx;   // column tiles of a row tile in turn
   const int m0 = by * RB_BM, n0 = (blockIdx.x - by * nx) * BN;
   const int kb = blockIdx.y * G.klen, ke = min(G.K, kb + G.klen);
-  Operand<TA, RB_BM, KADJ> A;
+  Operand<TA, RB_BM, KADJ, VEC> A;
   A.p = (const TA *)G.a; A.ld = G.lda; A.rows = G.M; A.r0 = m0; A.von = G.von;
-  Operand<float, BN, KADJ> B;
+  Operand<float, BN, KADJ, VEC> B;
   B.p = G.b; B.ld = G.ldb; B.rows = G.N; B.r0 = n0; B.von = KADJ ? nullptr : G.von;
-  A.vec = ((((uintptr_t)G.a) | (G.lda * sizeof(TA))) & 15) == 0 && ke % 4 == 0;
-  B.vec = ((((uintptr_t)G.b) | (G.ldb * 4)) & 15) == 0 && ke % 4 == 0;
   A.init();
   B.init();
   f32x4_t acc[4][NF] = {};
-  float cs[Operand<float, BN, KADJ>::IT] = {};
+  float cs[Operand<float, BN, KADJ, VEC>::IT] = {};
   const int get = lr * 64 + ((lg ^ (lr >> 2)) & 3) * 16;
   A.load(kb, ke);
   B.load(kb, ke);
@@ -376,7 +394,7 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
       float *red = reinterpret_cast<float *>(lds);
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < Operand<float, BN, KADJ>::IT; ++i) red[B.chunk(i) * BN + B.row(i)] = cs[i];
+      for (int i = 0; i < Operand<float, BN, KADJ, VEC>::IT; ++i) red[B.chunk(i) * BN + B.row(i)] = cs[i];
       __syncthreads();
       if (tid < BN && n0 + tid < G.N) {
         float s = 0.f;
@@ -463,8 +481,11 @@ template <typename TX> static void router_bwd(const void *x, const float *w, con
     RouterGemmArgs G{dl, (size_t)E, w, (size_t)E, T, d, E, ceil_div_h(E, RB_KS) * RB_KS, valid,
                      dx_in, dx, nullptr};
     const unsigned grid = (unsigned)ceil_div_h(d, 128) * ceil_div_h(T, RB_BM);
-    if constexpr (f32) router_gemm_kernel<float, float, 128, true, 3, 3><<<grid, 256, 0, st>>>(G);
-    else router_gemm_kernel<float, bf16_t, 128, true, 2, 2><<<grid, 256, 0, st>>>(G);
+    constexpr int P = f32 ? 3 : 2;
+    if (E % 4 == 0 && (((uintptr_t)dl | (uintptr_t)w) & 15) == 0)
+      router_gemm_kernel<float, TX, 128, true, true, P, P><<<grid, 256, 0, st>>>(G);
+    else
+      router_gemm_kernel<float, TX, 128, true, false, P, P><<<grid, 256, 0, st>>>(G);
   }
   if (dw) {
     const RouterSplit S = router_split(T, d, E);
@@ -475,8 +496,8 @@ template <typename TX> static void router_bwd(const void *x, const float *w, con
                      db ? cpart : nullptr};
     const dim3 grid(ceil_div_h(E, S.bn) * ceil_div_h(d, RB_BM), S.z);
     constexpr int PX = f32 ? 3 : 1;
-    if (S.bn == 64) router_gemm_kernel<TX, float, 64, false, PX, 3><<<grid, 256, 0, st>>>(G);
-    else router_gemm_kernel<TX, float, 128, false, PX, 3><<<grid, 256, 0, st>>>(G);
+    if (S.bn == 64) router_gemm_kernel<TX, float, 64, false, false, PX, 3><<<grid, 256, 0, st>>>(G);
+    else router_gemm_kernel<TX, float, 128, false, false, PX, 3><<<grid, 256, 0, st>>>(G);
     if (S.z > 1)
       router_sum_kernel<<<(unsigned)((n + 1023) / 1024 + (E + 255) / 256), 256, 0, st>>>(
           part, cpart, S.z, n, E, dw, db);

@@ -144,6 +144,14 @@ void launch_gate_bwd(bool bf16, const void *dy, const void *e_out, const int32_t
 // takes eight rows of one column; neighbouring threads neighbouring columns).
 constexpr int RB_BM = 128, RB_KS = 32;
 
+// An operand in LDS: planes of 64-byte rows.  Chunk c (16 bytes) of row r
+// stands at place c ^ ((r >> 1) + (r >> 3 & 1)) & 3: 16 lanes reading one chunk of
+// 16 rows, and 8 lanes writing one chunk of 8 rows, touch every bank once.
+DEV int rb_swz(int r) { return (r >> 1) + ((r >> 3) & 1); }
+DEV uint8_t *rb_place(uint8_t *lds, int r, int c) {
+  return lds + r * 64 + ((c ^ rb_swz(r)) & 3) * 16;
+}
+
 template <int P> struct Planes { uint4 v[P]; };
 
 // 8 values -> planes
@@ -248,12 +256,7 @@ template <typename T, int R, bool KADJ, bool VEC> struct Operand {
     else ok = ok && r0 + row(i) < rows && (!von || on[i][u]);
     return ok;
   }
-  DEV static uint8_t *place(uint8_t *lds, int r, int c) {
-    return lds + r * 64 + ((c ^ (r >> 2)) & 3) * 16;
-  }
-  // planes of 64-byte rows; chunk c of row r at place c ^ (r >> 2) & 3, so that
-  // 16 lanes reading one chunk of 16 rows touch every bank once.  sum: the
-  // items' values added up
+  // sum: the items' values added up
   template <int P> DEV void store(uint8_t *lds, float *sum = nullptr) {
     if (!whole()) {
 #pragma unroll
@@ -272,8 +275,9 @@ template <typename T, int R, bool KADJ, bool VEC> struct Operand {
           lo[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
           hi[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
         }
-        *reinterpret_cast<uint4 *>(place(lds, row(i), chunk(i))) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<uint4 *>(place(lds, row(i) + 1, chunk(i))) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        // (even columns in the first half of the rows, odd ones in the second)
+        *reinterpret_cast<uint4 *>(rb_place(lds, row(i) / 2, chunk(i))) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4 *>(rb_place(lds, row(i) / 2 + R / 2, chunk(i))) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       } else {
         if (sum) {
 #pragma unroll
@@ -282,7 +286,7 @@ template <typename T, int R, bool KADJ, bool VEC> struct Operand {
         const Planes<P> S = split8<P>(v[i]);
 #pragma unroll
         for (int q = 0; q < P; ++q)
-          *reinterpret_cast<uint4 *>(place(lds + q * R * 64, row(i), chunk(i))) = S.v[q];
+          *reinterpret_cast<uint4 *>(rb_place(lds + q * R * 64, row(i), chunk(i))) = S.v[q];
       }
     }
   }
@@ -315,7 +319,7 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
   B.init();
   f32x4_t acc[4][NF] = {};
   float cs[Operand<float, BN, KADJ, VEC>::IT] = {};
-  const int get = lr * 64 + ((lg ^ (lr >> 2)) & 3) * 16;
+  const int get = lr * 64 + ((lg ^ rb_swz(lr)) & 3) * 16;
   A.load(kb, ke);
   B.load(kb, ke);
   for (int k = kb, g = 0; k < ke; k += RB_KS, g ^= 1) {
@@ -335,18 +339,28 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
 #pragma unroll
       for (int m = 0; m < 4; ++m)
         av[p][m] = *reinterpret_cast<const uint4 *>(slot + (p * RB_BM + 64 * wm + 16 * m) * 64 + get);
+    // B's fragments are read two ahead of their products (left alone, the
+    // scheduler reads each one right before its use and waits)
+    uint4 bv[3];
+    auto read_b = [&](int s) {
+      bv[s % 3] = *reinterpret_cast<const uint4 *>(
+          sb + (s / NF * BN + (BN / 2) * wn + 16 * (s % NF)) * 64 + get);
+    };
+    read_b(0);
+    read_b(1);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int p = 0; p < PB; ++p)
+    for (int s = 0; s < PB * NF; ++s) {
+      if (s + 2 < PB * NF) read_b(s + 2);
 #pragma unroll
-      for (int n = 0; n < NF; ++n) {
-        const uint4 bv = *reinterpret_cast<const uint4 *>(sb + (p * BN + (BN / 2) * wn + 16 * n) * 64 + get);
+      for (int q = 0; q < PA; ++q)
+        if (s / NF + q < PM) {
 #pragma unroll
-        for (int q = 0; q < PA; ++q)
-          if (p + q < PM) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) acc[m][n] = mfma32(bv, av[q][m], acc[m][n]);
-          }
-      }
+          for (int m = 0; m < 4; ++m)
+            acc[m][s % NF] = mfma32(bv[s % 3], av[q][m], acc[m][s % NF]);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
   // a lane has columns n0 + .. + 4 lg + 0..3 of row lr of each fragment
   TC *out = (TC *)G.out + (size_t)blockIdx.y * G.M * G.N;
@@ -354,7 +368,8 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
   const bool vec = G.N % 4 == 0 && (((uintptr_t)out | (uintptr_t)add) & (4 * sizeof(TC) - 1)) == 0;
 #pragma unroll
   for (int m = 0; m < 4; ++m) {
-    const int r = m0 + 64 * wm + 16 * m + lr;
+    const int rl = 16 * m + lr;   // row of the wave's 64: see Operand for pairs
+    const int r = m0 + (Operand<TA, RB_BM, KADJ, VEC>::PAIR ? 2 * rl + wm : 64 * wm + rl);
     if (r >= G.M) continue;
 #pragma unroll
     for (int n = 0; n < NF; ++n) {

@@ -185,19 +185,25 @@ template <int P> DEV Planes<P> split8(const float *f) {
 // pair of rows of bf16 with k as the row index) and an 8-wide chunk of k; IT
 // items per thread.  load() only asks memory (addresses held inside the
 // operand, no condition on a value); what lies outside or is masked becomes 0
-// in store(), which asks only where a step is not whole.  VEC: k adjacent,
-// rows at multiples of 16 bytes, k1 a multiple of 4.
+// in store(), which asks only where a step is not whole.  Two steps are on
+// their way at once (Step).  VEC: k adjacent, rows at multiples of 16 bytes,
+// k1 a multiple of 4.
 template <typename T, int R, bool KADJ, bool VEC> struct Operand {
   static constexpr bool PAIR = !KADJ && sizeof(T) == 2;
   static constexpr int IT = R * 4 / 256 / (PAIR ? 2 : 1), RI = R / (PAIR ? 2 : 1);
   const T *p;           // [rows][ld] (KADJ) or [k][ld]
   size_t ld;
-  int rows, r0;
+  int rows, r0, k1;     // values of k at k1 and behind are 0
   const uint8_t *von;   // mask over k (not KADJ) or over the rows (KADJ), or null
-  int k0, k1;           // the step on its way: [k0, k0 + 32), those at k1 and behind are 0
-  float v[IT][8];       // (PAIR: the bits of two bf16 columns)
-  uint8_t on[IT][8];    // masks of the step (not KADJ), or of the rows ([.][0])
   const T *at[IT];      // KADJ: the rows
+  bool row_on[IT];      // and whether they take part
+  uint32_t off[IT][8];  // not KADJ: byte offsets of the 8 values from row k0 of a step
+
+  struct Step {         // [k0, k0 + 32)
+    int k0;
+    float v[IT][8];     // (PAIR: the bits of two bf16 columns)
+    uint8_t on[IT][8];  // not KADJ: masks
+  };
 
   DEV int row(int i) const {
     return KADJ ? (threadIdx.x >> 2) + 64 * i : (threadIdx.x + 256 * i) % RI * (PAIR ? 2 : 1);
@@ -206,63 +212,76 @@ template <typename T, int R, bool KADJ, bool VEC> struct Operand {
     return KADJ ? threadIdx.x & 3 : __builtin_amdgcn_readfirstlane((threadIdx.x + 256 * i) / RI);
   }
   DEV void init() {
-    if constexpr (KADJ) {
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        const int r = min(r0 + row(i), rows - 1);
-        at[i] = p + (size_t)r * ld;
-        on[i][0] = r0 + row(i) < rows && (!von || von[r]);
-      }
-    }
-  }
-  DEV void load(int k0_, int k1_) {
-    k0 = k0_;
-    k1 = k1_;
-    if constexpr (!KADJ) {
-      if (von) {
-#pragma unroll
-        for (int i = 0; i < IT; ++i)
-#pragma unroll
-          for (int u = 0; u < 8; ++u) on[i][u] = von[min(k0 + 8 * chunk(i) + u, k1 - 1)];
-      }
-    }
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int k = k0 + 8 * chunk(i);
-      if constexpr (KADJ && VEC) {
-        static_assert(sizeof(T) == 4, "float32 rows");
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 a = *reinterpret_cast<const float4 *>(at[i] + min(k + 4 * h, k1 - 4));
-          v[i][4 * h] = a.x; v[i][4 * h + 1] = a.y; v[i][4 * h + 2] = a.z; v[i][4 * h + 3] = a.w;
-        }
-      } else if constexpr (KADJ) {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[i][u] = at[i][min(k + u, k1 - 1)];
+      if constexpr (KADJ) {
+        const int r = min(r0 + row(i), rows - 1);
+        at[i] = p + (size_t)r * ld;
+        row_on[i] = r0 + row(i) < rows && (!von || von[r]);
       } else {
         // (PAIR: rows and ld are even, the pair is one aligned word)
         const uint32_t r = min(r0 + row(i), rows - (PAIR ? 2 : 1));
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          v[i][u] = *reinterpret_cast<const float *>((p + (size_t)min(k + u, k1 - 1) * ld) + r);
+          off[i][u] = ((8 * chunk(i) + u) * (uint32_t)ld + r) * (uint32_t)sizeof(T);
       }
     }
   }
-  // whether nothing of the step is outside or masked
-  DEV bool whole() const { return k0 + RB_KS <= k1 && r0 + R <= rows && !von; }
-  DEV bool inside(int i, int u) const {
-    bool ok = k0 + 8 * chunk(i) + u < k1;
-    if constexpr (KADJ) ok = ok && on[i][0];
-    else ok = ok && r0 + row(i) < rows && (!von || on[i][u]);
-    return ok;
-  }
-  // sum: the items' values added up
-  template <int P> DEV void store(uint8_t *lds, float *sum = nullptr) {
-    if (!whole()) {
+  DEV void load(Step &S, int k0) const {
+    S.k0 = k0;
+    if constexpr (!KADJ) {
+      if (von) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+#pragma unroll
+          for (int u = 0; u < 8; ++u) S.on[i][u] = von[min(k0 + 8 * chunk(i) + u, k1 - 1)];
+      }
+      const char *base = reinterpret_cast<const char *>(p + (size_t)min(k0, k1 - 1) * ld);
+      // the last step may end early: its rows behind the end are the last row
+      const uint32_t most = (uint32_t)max(k1 - 1 - k0, 0), rb = (uint32_t)(ld * sizeof(T));
+      const bool cut = most < RB_KS - 1;
 #pragma unroll
       for (int i = 0; i < IT; ++i)
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[i][u] = inside(i, u) ? v[i][u] : 0.f;
+        for (int u = 0; u < 8; ++u) {
+          uint32_t o = off[i][u];
+          if (cut) {
+            const uint32_t q = 8 * chunk(i) + u;
+            o -= (q - min(q, most)) * rb;
+          }
+          S.v[i][u] = *reinterpret_cast<const float *>(base + (size_t)o);
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int k = k0 + 8 * chunk(i);
+        if constexpr (VEC) {
+          static_assert(sizeof(T) == 4, "float32 rows");
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 a = *reinterpret_cast<const float4 *>(at[i] + min(k + 4 * h, k1 - 4));
+            S.v[i][4 * h] = a.x; S.v[i][4 * h + 1] = a.y;
+            S.v[i][4 * h + 2] = a.z; S.v[i][4 * h + 3] = a.w;
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) S.v[i][u] = at[i][min(k + u, k1 - 1)];
+        }
+      }
+    }
+  }
+  // sum: the items' values added up
+  template <int P> DEV void store(Step &S, uint8_t *lds, float *sum = nullptr) const {
+    if (S.k0 + RB_KS > k1 || r0 + R > rows || von) {   // not all of the step takes part
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          bool ok = S.k0 + 8 * chunk(i) + u < k1;
+          if constexpr (KADJ) ok = ok && row_on[i];
+          else ok = ok && r0 + row(i) < rows && (!von || S.on[i][u]);
+          S.v[i][u] = ok ? S.v[i][u] : 0.f;
+        }
     }
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
@@ -271,7 +290,7 @@ template <typename T, int R, bool KADJ, bool VEC> struct Operand {
         uint32_t lo[4], hi[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t x = __float_as_uint(v[i][2 * j]), y = __float_as_uint(v[i][2 * j + 1]);
+          const uint32_t x = __float_as_uint(S.v[i][2 * j]), y = __float_as_uint(S.v[i][2 * j + 1]);
           lo[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
           hi[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
         }
@@ -281,12 +300,12 @@ template <typename T, int R, bool KADJ, bool VEC> struct Operand {
       } else {
         if (sum) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) sum[i] += v[i][u];
+          for (int u = 0; u < 8; ++u) sum[i] += S.v[i][u];
         }
-        const Planes<P> S = split8<P>(v[i]);
+        const Planes<P> Q = split8<P>(S.v[i]);
 #pragma unroll
         for (int q = 0; q < P; ++q)
-          *reinterpret_cast<uint4 *>(rb_place(lds + q * R * 64, row(i), chunk(i))) = S.v[q];
+          *reinterpret_cast<uint4 *>(rb_place(lds + q * R * 64, row(i), chunk(i))) = Q.v[q];
       }
     }
   }
@@ -311,25 +330,27 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
   const int nx = (G.N + BN - 1) / BN, by = blockIdx.x / nx;   // column tiles of a row tile in turn
   const int m0 = by * RB_BM, n0 = (blockIdx.x - by * nx) * BN;
   const int kb = blockIdx.y * G.klen, ke = min(G.K, kb + G.klen);
-  Operand<TA, RB_BM, KADJ, VEC> A;
-  A.p = (const TA *)G.a; A.ld = G.lda; A.rows = G.M; A.r0 = m0; A.von = G.von;
-  Operand<float, BN, KADJ, VEC> B;
-  B.p = G.b; B.ld = G.ldb; B.rows = G.N; B.r0 = n0; B.von = KADJ ? nullptr : G.von;
+  using OA = Operand<TA, RB_BM, KADJ, VEC>;
+  using OB = Operand<float, BN, KADJ, VEC>;
+  OA A;
+  A.p = (const TA *)G.a; A.ld = G.lda; A.rows = G.M; A.r0 = m0; A.k1 = ke; A.von = G.von;
+  OB B;
+  B.p = G.b; B.ld = G.ldb; B.rows = G.N; B.r0 = n0; B.k1 = ke; B.von = KADJ ? nullptr : G.von;
   A.init();
   B.init();
   f32x4_t acc[4][NF] = {};
-  float cs[Operand<float, BN, KADJ, VEC>::IT] = {};
+  float cs[OB::IT] = {};
   const int get = lr * 64 + ((lg ^ rb_swz(lr)) & 3) * 16;
-  A.load(kb, ke);
-  B.load(kb, ke);
-  for (int k = kb, g = 0; k < ke; k += RB_KS, g ^= 1) {
+  // one step from slot g: its values into LDS, the step after the next one
+  // asked for, then the products
+  auto step = [&](typename OA::Step &SA, typename OB::Step &SB, int k, int g) {
     uint8_t *slot = lds + g * SLOT, *sb = slot + PA * RB_BM * 64;
-    A.template store<PA>(slot);
-    B.template store<PB>(sb, KADJ ? nullptr : cs);
+    A.template store<PA>(SA, slot);
+    B.template store<PB>(SB, sb, KADJ ? nullptr : cs);
     __builtin_amdgcn_sched_barrier(0);
-    if (k + RB_KS < ke) {
-      A.load(k + RB_KS, ke);
-      B.load(k + RB_KS, ke);
+    if (k + 2 * RB_KS < ke) {
+      A.load(SA, k + 2 * RB_KS);
+      B.load(SB, k + 2 * RB_KS);
     }
     __builtin_amdgcn_s_waitcnt(0xC07F);   // (LDS only: the loads stay in flight)
     block_barrier();
@@ -361,6 +382,16 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
         }
       __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  typename OA::Step a0, a1;
+  typename OB::Step b0, b1;
+  A.load(a0, kb);
+  B.load(b0, kb);
+  A.load(a1, kb + RB_KS);
+  B.load(b1, kb + RB_KS);
+  for (int k = kb; k < ke; k += 2 * RB_KS) {
+    step(a0, b0, k, 0);
+    if (k + RB_KS < ke) step(a1, b1, k + RB_KS, 1);
   }
   // a lane has columns n0 + .. + 4 lg + 0..3 of row lr of each fragment
   TC *out = (TC *)G.out + (size_t)blockIdx.y * G.M * G.N;
@@ -369,7 +400,7 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
 #pragma unroll
   for (int m = 0; m < 4; ++m) {
     const int rl = 16 * m + lr;   // row of the wave's 64: see Operand for pairs
-    const int r = m0 + (Operand<TA, RB_BM, KADJ, VEC>::PAIR ? 2 * rl + wm : 64 * wm + rl);
+    const int r = m0 + (OA::PAIR ? 2 * rl + wm : 64 * wm + rl);
     if (r >= G.M) continue;
 #pragma unroll
     for (int n = 0; n < NF; ++n) {
@@ -409,7 +440,7 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
       float *red = reinterpret_cast<float *>(lds);
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < Operand<float, BN, KADJ, VEC>::IT; ++i) red[B.chunk(i) * BN + B.row(i)] = cs[i];
+      for (int i = 0; i < OB::IT; ++i) red[B.chunk(i) * BN + B.row(i)] = cs[i];
       __syncthreads();
       if (tid < BN && n0 + tid < G.N) {
         float s = 0.f;

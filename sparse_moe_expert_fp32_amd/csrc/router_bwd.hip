@@ -152,45 +152,40 @@ DEV uint8_t *rb_place(uint8_t *lds, int r, int c) {
   return lds + r * 64 + ((c ^ rb_swz(r)) & 3) * 16;
 }
 
-template <int P> struct Planes { uint4 v[P]; };
-
-// 8 values -> planes
-template <int P> DEV Planes<P> split8(const float *f) {
-  Planes<P> S;
-  float r[8];
+// W values -> planes of W bf16 (W / 2 words each)
+template <int P, int W> DEV void split(const float *f, uint32_t (&o)[P][W / 2]) {
+  float r[W];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = f[i];
+  for (int i = 0; i < W; ++i) r[i] = f[i];
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    uint32_t o[4];
+  for (int p = 0; p < P; ++p)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < W / 2; ++i) {
       const uint32_t lo = __float_as_uint(r[2 * i]), hi = __float_as_uint(r[2 * i + 1]);
       if (p == 1 && P == 2) {
-        o[i] = cvt_pk_bf16(r[2 * i], r[2 * i + 1]);
+        o[p][i] = cvt_pk_bf16(r[2 * i], r[2 * i + 1]);
       } else {
-        o[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);   // the upper halves
+        o[p][i] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);   // the upper halves
         if (p + 1 < P) {
           r[2 * i] -= __uint_as_float(lo & 0xFFFF0000u);
           r[2 * i + 1] -= __uint_as_float(hi & 0xFFFF0000u);
         }
       }
     }
-    S.v[p] = make_uint4(o[0], o[1], o[2], o[3]);
-  }
-  return S;
 }
 
-// One operand of a block: R rows (m or n) from r0 on.  Thread items: a row (a
-// pair of rows of bf16 with k as the row index) and an 8-wide chunk of k; IT
-// items per thread.  load() only asks memory (addresses held inside the
+// One operand of a block: R rows (m or n) from r0 on.  Thread items, IT per
+// thread: with k adjacent a row and 4 values of k (8 threads ask for a whole
+// 128-byte piece of a row); with k as the row index a row (bf16: a pair of
+// rows) and 8 values of k.  load() only asks memory (addresses held inside the
 // operand, no condition on a value); what lies outside or is masked becomes 0
 // in store(), which asks only where a step is not whole.  Two steps are on
 // their way at once (Step).  VEC: k adjacent, rows at multiples of 16 bytes,
 // k1 a multiple of 4.
 template <typename T, int R, bool KADJ, bool VEC> struct Operand {
   static constexpr bool PAIR = !KADJ && sizeof(T) == 2;
-  static constexpr int IT = R * 4 / 256 / (PAIR ? 2 : 1), RI = R / (PAIR ? 2 : 1);
+  static constexpr int W = KADJ ? 4 : 8;   // values of an item
+  static constexpr int IT = R * RB_KS / W / 256 / (PAIR ? 2 : 1), RI = R / (PAIR ? 2 : 1);
   const T *p;           // [rows][ld] (KADJ) or [k][ld]
   size_t ld;
   int rows, r0, k1;     // values of k at k1 and behind are 0
@@ -201,15 +196,15 @@ template <typename T, int R, bool KADJ, bool VEC> struct Operand {
 
   struct Step {         // [k0, k0 + 32)
     int k0;
-    float v[IT][8];     // (PAIR: the bits of two bf16 columns)
-    uint8_t on[IT][8];  // not KADJ: masks
+    float v[IT][W];     // (PAIR: the bits of two bf16 columns)
+    uint8_t on[IT][W];  // not KADJ: masks
   };
 
   DEV int row(int i) const {
-    return KADJ ? (threadIdx.x >> 2) + 64 * i : (threadIdx.x + 256 * i) % RI * (PAIR ? 2 : 1);
+    return KADJ ? (threadIdx.x >> 3) + 32 * i : (threadIdx.x + 256 * i) % RI * (PAIR ? 2 : 1);
   }
-  DEV int chunk(int i) const {   // not KADJ: the same in a whole wave
-    return KADJ ? threadIdx.x & 3 : __builtin_amdgcn_readfirstlane((threadIdx.x + 256 * i) / RI);
+  DEV int chunk(int i) const {   // k / W; not KADJ: the same in a whole wave
+    return KADJ ? threadIdx.x & 7 : __builtin_amdgcn_readfirstlane((threadIdx.x + 256 * i) / RI);
   }
   DEV void init() {
 #pragma unroll
@@ -254,18 +249,14 @@ template <typename T, int R, bool KADJ, bool VEC> struct Operand {
     } else {
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
-        const int k = k0 + 8 * chunk(i);
+        static_assert(!KADJ || sizeof(T) == 4, "float32 rows");
+        const int k = k0 + W * chunk(i);
         if constexpr (VEC) {
-          static_assert(sizeof(T) == 4, "float32 rows");
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 a = *reinterpret_cast<const float4 *>(at[i] + min(k + 4 * h, k1 - 4));
-            S.v[i][4 * h] = a.x; S.v[i][4 * h + 1] = a.y;
-            S.v[i][4 * h + 2] = a.z; S.v[i][4 * h + 3] = a.w;
-          }
+          const float4 a = *reinterpret_cast<const float4 *>(at[i] + min(k, k1 - 4));
+          S.v[i][0] = a.x; S.v[i][1] = a.y; S.v[i][2] = a.z; S.v[i][3] = a.w;
         } else {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) S.v[i][u] = at[i][min(k + u, k1 - 1)];
+          for (int u = 0; u < W; ++u) S.v[i][u] = at[i][min(k + u, k1 - 1)];
         }
       }
     }
@@ -276,8 +267,8 @@ template <typename T, int R, bool KADJ, bool VEC> struct Operand {
 #pragma unroll
       for (int i = 0; i < IT; ++i)
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          bool ok = S.k0 + 8 * chunk(i) + u < k1;
+        for (int u = 0; u < W; ++u) {
+          bool ok = S.k0 + W * chunk(i) + u < k1;
           if constexpr (KADJ) ok = ok && row_on[i];
           else ok = ok && r0 + row(i) < rows && (!von || S.on[i][u]);
           S.v[i][u] = ok ? S.v[i][u] : 0.f;
@@ -300,12 +291,20 @@ template <typename T, int R, bool KADJ, bool VEC> struct Operand {
       } else {
         if (sum) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) sum[i] += S.v[i][u];
+          for (int u = 0; u < W; ++u) sum[i] += S.v[i][u];
         }
-        const Planes<P> Q = split8<P>(S.v[i]);
+        uint32_t o[P][W / 2];
+        split<P, W>(S.v[i], o);
 #pragma unroll
-        for (int q = 0; q < P; ++q)
-          *reinterpret_cast<uint4 *>(rb_place(lds + q * R * 64, row(i), chunk(i))) = Q.v[q];
+        for (int q = 0; q < P; ++q) {
+          uint8_t *pl = lds + q * R * 64;
+          if constexpr (KADJ)
+            *reinterpret_cast<uint2 *>(rb_place(pl, row(i), chunk(i) >> 1) + 8 * (chunk(i) & 1)) =
+                make_uint2(o[q][0], o[q][1]);
+          else
+            *reinterpret_cast<uint4 *>(rb_place(pl, row(i), chunk(i))) =
+                make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
+        }
       }
     }
   }

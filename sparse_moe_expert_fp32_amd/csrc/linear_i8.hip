@@ -290,7 +290,8 @@ template <typename T, int MF, int NW> static void launch_short(const LinearI8Arg
 // fragments a wave has (32 MI rows); a tile runs as the smallest class that
 // holds its rows.
 constexpr int BG_BM = 256, BG_BN = 128, BG_KS = 128;
-constexpr int BG_A = BG_BM * BG_KS, BG_LDS = BG_A + BG_BN * BG_KS;   // bytes
+constexpr int BG_A = BG_BM * BG_KS, BG_SCALES = BG_A + BG_BN * BG_KS;   // bytes
+constexpr int BG_LDS = BG_SCALES + (BG_BM + BG_BN) * 4;   // with the tile's row and channel scales
 
 // Rows of 128 bytes in LDS.  Chunk c (16 bytes) of row r stands at place
 // c ^ (r >> 1) & 7 for the rows of a, whose fragments read 16 adjacent rows,
@@ -374,6 +375,12 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
     }
   };
   load(0);
+  // the tile's scales wait in LDS for its end (the first barrier shows them)
+  float *scales = reinterpret_cast<float *>(lds + BG_SCALES);
+  scales[tid] = A.a_scale[source_row(A, min(R.p0 + tid, R.end - 1))];
+  if (tid < BG_BN)
+    scales[BG_BM + tid] =
+        A.w_scale ? A.w_scale[(size_t)R.e * A.N + min(n0 + tid, A.N - 1)] : 1.0f;
   for (int j = 0; j < steps; ++j) {
     store();
     __builtin_amdgcn_sched_barrier(0);   // (the registers are free again)
@@ -385,19 +392,15 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
     __builtin_amdgcn_sched_barrier(0);
   }
   const bool vec = (((uintptr_t)A.out & 15) | ((A.ldo * sizeof(T)) & 15)) == 0;
-  float sw[4][4];
+  f32x4_t sw[4];
 #pragma unroll
   for (int f = 0; f < 4; ++f)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int n = n0 + 64 * wn + gt_col(f, 4 * lg) + c;
-      sw[f][c] = A.w_scale ? A.w_scale[(size_t)R.e * A.N + min(n, A.N - 1)] : 1.0f;
-    }
+    sw[f] = *reinterpret_cast<const f32x4_t *>(scales + BG_BM + 64 * wn + gt_col(f, 4 * lg));
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int p = R.p0 + 16 * (2 * i + wm) + lr;
+    const int pl = 16 * (2 * i + wm) + lr, p = R.p0 + pl;
     if (p >= R.end) continue;
-    const float sa = A.a_scale[source_row(A, p)];
+    const float sa = scales[pl];
     T *out = (T *)A.out + (size_t)p * A.ldo;
 #pragma unroll
     for (int f = 0; f < 4; f += 2) {   // 8 adjacent channels

@@ -396,40 +396,57 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
   TC *out = (TC *)G.out + (size_t)blockIdx.y * G.M * G.N;
   const TC *add = (const TC *)G.add;
   const bool vec = G.N % 4 == 0 && (((uintptr_t)out | (uintptr_t)add) & (4 * sizeof(TC) - 1)) == 0;
+  auto row_of = [&](int m) {   // see Operand for pairs
+    const int rl = 16 * m + lr;
+    return m0 + (OA::PAIR ? 2 * rl + wm : 64 * wm + rl);
+  };
+  auto col_of = [&](int n) { return n0 + (BN / 2) * wn + 16 * n + 4 * lg; };
+  if (add) {   // every load in flight before the first sum
+    TC old[4][NF][4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int n = 0; n < NF; ++n) {
+        const TC *q = add + (size_t)min(row_of(m), G.M - 1) * G.N;
+        if (vec) {   // (N is a multiple of 4: the four columns are there, or the last four)
+          const int c = min(col_of(n), G.N - 4);
+          if constexpr (sizeof(TC) == 2)
+            *reinterpret_cast<uint2 *>(old[m][n]) = *reinterpret_cast<const uint2 *>(q + c);
+          else
+            *reinterpret_cast<float4 *>(old[m][n]) = *reinterpret_cast<const float4 *>(q + c);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) old[m][n][i] = q[min(col_of(n) + i, G.N - 1)];
+        }
+      }
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int n = 0; n < NF; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][n][i] += Elem<TC>::ld(old[m][n], i);
+  }
 #pragma unroll
   for (int m = 0; m < 4; ++m) {
-    const int rl = 16 * m + lr;   // row of the wave's 64: see Operand for pairs
-    const int r = m0 + (OA::PAIR ? 2 * rl + wm : 64 * wm + rl);
+    const int r = row_of(m);
     if (r >= G.M) continue;
 #pragma unroll
     for (int n = 0; n < NF; ++n) {
-      const int c = n0 + (BN / 2) * wn + 16 * n + 4 * lg;
-      const size_t o = (size_t)r * G.N + c;
+      const int c = col_of(n);
+      TC *q = out + (size_t)r * G.N + c;
       if (c >= G.N) continue;
-      float v[4] = {acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]};
-      if (vec) {   // (N is a multiple of 4: the four columns are there)
-        if constexpr (sizeof(TC) == 2) {
-          if (add) {
-            const uint2 d = *reinterpret_cast<const uint2 *>(add + o);
-            v[0] += __uint_as_float(d.x << 16); v[1] += __uint_as_float(d.x & 0xFFFF0000u);
-            v[2] += __uint_as_float(d.y << 16); v[3] += __uint_as_float(d.y & 0xFFFF0000u);
-          }
-          *reinterpret_cast<uint2 *>(out + o) =
-              make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
-        } else {
-          if (add) {
-            const float4 d = *reinterpret_cast<const float4 *>(add + o);
-            v[0] += d.x; v[1] += d.y; v[2] += d.z; v[3] += d.w;
-          }
-          *reinterpret_cast<float4 *>(out + o) = make_float4(v[0], v[1], v[2], v[3]);
-        }
+      const f32x4_t v = acc[m][n];
+      if (vec) {
+        if constexpr (sizeof(TC) == 2)
+          *reinterpret_cast<uint2 *>(q) = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
+        else
+          *reinterpret_cast<float4 *>(q) = make_float4(v[0], v[1], v[2], v[3]);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (c + i < G.N) {
-            const float s = v[i] + (add ? Elem<TC>::ld(add, o + i) : 0.f);
-            if constexpr (sizeof(TC) == 2) out[o + i] = (uint16_t)cvt_pk_bf16(s, s);
-            else out[o + i] = s;
+            if constexpr (sizeof(TC) == 2) q[i] = (uint16_t)cvt_pk_bf16(v[i], v[i]);
+            else q[i] = v[i];
           }
       }
     }

@@ -21,13 +21,16 @@
 
 namespace moe {
 
+// Nearest whole number of v / s, ties to even (inv: 1 / s).
 DEV int quant_round(float v, float s, float inv) {
-  float q = rintf(v * inv);
+  const float q = rintf(v * inv);
   const float r = fmaf(-q, s, v);          // exact: |r| <= about s
-  const float h = 0.5f * s, ar = fabsf(r);
-  const bool odd = ((int)q & 1) != 0;
-  if (ar > h || (ar == h && odd)) q += r > 0.f ? 1.f : -1.f;
-  return (int)fminf(fmaxf(q, -127.f), 127.f);
+  const int i = (int)q;
+  // one step towards v if |r| > s / 2, or |r| = s / 2 and q is odd: for odd q
+  // the border is the float below s / 2
+  const float h = __uint_as_float(__float_as_uint(0.5f * s) - (uint32_t)(i & 1));
+  const int step = fabsf(r) > h ? (__float_as_int(r) >> 31) | 1 : 0;
+  return min(max(i + step, -127), 127);
 }
 
 // The expert of row p: the number of experts that end at or before it.  All
@@ -70,24 +73,26 @@ template <typename T, bool VEC> DEV void load8(const T *p, int c, int K, float *
   }
 }
 
-template <typename T, int NT, int NH, bool VEC>
+template <typename T, int NT, int NH, bool VEC, bool SWIGLU>
 __global__ __launch_bounds__(256) void quant_i8_kernel(QuantArgs A) {
   constexpr int RB = 256 / NT;              // rows per block
   __shared__ uint32_t red[4];
   const int tid = threadIdx.x % NT, p = A.p0 + blockIdx.x * RB + threadIdx.x / NT;
   if (p >= A.p0 + A.M || (A.offsets && p >= A.offsets[A.E])) return;   // (NT = 256: the whole block)
   const T *x = (const T *)A.x + (size_t)p * A.ldx;
-  const T *u = A.u ? (const T *)A.u + (size_t)p * A.ldu : nullptr;
+  const T *u = (const T *)A.u + (SWIGLU ? (size_t)p * A.ldu : 0);
   const float *cs = nullptr;
   if (A.col_scale)
     cs = A.col_scale + (size_t)(A.offsets ? expert_of_row(A.offsets, A.E, p) : 0) * A.K;
   auto value = [&](int c, float *v) {
     load8<T, VEC>(x, c, A.K, v);
-    if (u) {
+    if constexpr (SWIGLU) {
+      // (the hardware's exponential and reciprocal: a few roundings of v)
       float m[8];
       load8<T, VEC>(u, c, A.K, m);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.0f + expf(-v[i])) * m[i];
+      for (int i = 0; i < 8; ++i)
+        v[i] *= __builtin_amdgcn_rcpf(1.0f + __expf(-v[i])) * m[i];
     }
     if (cs) {
       float m[8];
@@ -152,9 +157,10 @@ __global__ __launch_bounds__(256) void quant_i8_kernel(QuantArgs A) {
 // four waves per row otherwise.
 constexpr int QU_WAVE_ROWS = 2048;
 
-template <typename T, bool VEC> static void quant_launch(const QuantArgs &A, hipStream_t st) {
+template <typename T, bool VEC, bool SWIGLU>
+static void quant_launch(const QuantArgs &A, hipStream_t st) {
 #define MOE_Q(NT, NH) \
-  quant_i8_kernel<T, NT, NH, VEC><<<(A.M + 256 / NT - 1) / (256 / NT), 256, 0, st>>>(A)
+  quant_i8_kernel<T, NT, NH, VEC, SWIGLU><<<(A.M + 256 / NT - 1) / (256 / NT), 256, 0, st>>>(A)
   const bool wave = A.M >= QU_WAVE_ROWS;
   if (wave && A.K <= 1024) MOE_Q(64, 2);
   else if (wave && A.K <= 2048) MOE_Q(64, 4);
@@ -162,6 +168,15 @@ template <typename T, bool VEC> static void quant_launch(const QuantArgs &A, hip
   else if (A.K <= 2048) MOE_Q(256, 1);
   else MOE_Q(256, 4);
 #undef MOE_Q
+}
+template <typename T> static void quant_launch(const QuantArgs &A, bool vec, hipStream_t st) {
+  if (A.u) {
+    if (vec) quant_launch<T, true, true>(A, st);
+    else quant_launch<T, false, true>(A, st);
+  } else {
+    if (vec) quant_launch<T, true, false>(A, st);
+    else quant_launch<T, false, false>(A, st);
+  }
 }
 
 void launch_quant_i8(bool bf16, const QuantArgs &all, hipStream_t st) {
@@ -180,11 +195,8 @@ void launch_quant_i8(bool bf16, const QuantArgs &all, hipStream_t st) {
                    (((uintptr_t)A.x | (uintptr_t)(A.ldx * ab)) & 15) == 0 &&
                    (!A.u || (((uintptr_t)A.u | (uintptr_t)(A.ldu * ab)) & 15) == 0) &&
                    ((uintptr_t)A.col_scale & 15) == 0;
-  if (bf16) {
-    if (vec) quant_launch<bf16_t, true>(A, st); else quant_launch<bf16_t, false>(A, st);
-  } else {
-    if (vec) quant_launch<float, true>(A, st); else quant_launch<float, false>(A, st);
-  }
+  if (bf16) quant_launch<bf16_t>(A, vec, st);
+  else quant_launch<float>(A, vec, st);
 }
 
 }  // namespace moe

@@ -290,8 +290,9 @@ template <typename T, int MF, int NW> static void launch_short(const LinearI8Arg
 // fragments a wave has (32 MI rows); a tile runs as the smallest class that
 // holds its rows.
 constexpr int BG_BM = 256, BG_BN = 128, BG_KS = 128;
-constexpr int BG_A = BG_BM * BG_KS, BG_SCALES = BG_A + BG_BN * BG_KS;   // bytes
-constexpr int BG_LDS = BG_SCALES + (BG_BM + BG_BN) * 4;   // with the tile's row and channel scales
+// bytes of LDS for tiles of up to BM rows: channels, row and channel scales, rows
+constexpr int BG_SCALES = BG_BN * BG_KS, BG_A = BG_SCALES + (BG_BM + BG_BN) * 4;
+constexpr int bg_lds(int BM) { return BG_A + BM * BG_KS; }
 
 // Rows of 128 bytes in LDS.  Chunk c (16 bytes) of row r stands at place
 // c ^ (r >> 1) & 7 for the rows of a, whose fragments read 16 adjacent rows,
@@ -310,11 +311,11 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
   const int w = tid >> 6, wm = w & 1, wn = w >> 1;
   const int tr = tid >> 3, tc = tid & 7;     // row and chunk of this thread's first piece
   const int steps = (A.K + BG_KS - 1) / BG_KS;   // (rows of a hold 0 behind K)
-  const int a_put = tr * BG_KS + (tc ^ bg_swz_a(tr)) * 16;
-  const int w_put = BG_A + tr * BG_KS + (tc ^ bg_swz_w(tr)) * 16;
+  const int a_put = BG_A + tr * BG_KS + (tc ^ bg_swz_a(tr)) * 16;
+  const int w_put = tr * BG_KS + (tc ^ bg_swz_w(tr)) * 16;
   const int ar = 16 * wm + lr, wr = 64 * wn + gt_col(0, lr);
-  const int a_get = ar * BG_KS + (lg ^ bg_swz_a(ar)) * 16;
-  const int w_get = BG_A + wr * BG_KS + (lg ^ bg_swz_w(wr)) * 16;
+  const int a_get = BG_A + ar * BG_KS + (lg ^ bg_swz_a(ar)) * 16;
+  const int w_get = wr * BG_KS + (lg ^ bg_swz_w(wr)) * 16;
   // byte offsets inside a and inside the matrix are below 2^32 (launch_linear)
   const int8_t *we = A.w + (size_t)R.e * A.N * A.ldw;
   uint32_t ao[MI], wo[4];
@@ -428,14 +429,15 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
 // Blocks go round the 8 XCDs in turn; each XCD takes a contiguous run of the
 // (row tile, channel tile) list, so that tiles that share rows and matrices
 // share its L2.  The run is an eighth of the tiles there are, not of the grid.
-template <typename T, int NC>
-__global__ __launch_bounds__(256, 2) void linear_i8_big_kernel(LinearI8Args A) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[BG_LDS];
+// BM: rows of a tile, 256 or, where those are too few to fill the chip, 64.
+template <typename T, int NC, int BM>
+__global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void linear_i8_big_kernel(LinearI8Args A) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[bg_lds(BM)];
   const int nt = (A.N + BG_BN - 1) / BG_BN;
   RowTile R;
   int n0;
   {
-    const TileList<BG_BM, NC> list(A.offsets, A.E, A.M);
+    const TileList<BM, NC> list(A.offsets, A.E, A.M);
     const int64_t items = (int64_t)list.count() * nt, run = (items + 7) / 8;
     const int64_t at = blockIdx.x >> 3, item = run * (blockIdx.x & 7) + at;
     if (at >= run || item >= items) return;
@@ -444,24 +446,27 @@ __global__ __launch_bounds__(256, 2) void linear_i8_big_kernel(LinearI8Args A) {
     if (!list.get(t, R)) return;
   }
   const int rows = R.end - R.p0;
-  if (rows <= 64) big_tile<T, 2>(A, R, n0, lds);
+  if (BM == 64 || rows <= 64) big_tile<T, 2>(A, R, n0, lds);
   else if (rows <= 128) big_tile<T, 4>(A, R, n0, lds);
   else if (rows <= 192) big_tile<T, 6>(A, R, n0, lds);
   else big_tile<T, 8>(A, R, n0, lds);
 }
 
-template <typename T> static void launch_big(const LinearI8Args &A, hipStream_t st) {
-  const int64_t tiles = A.offsets ? A.M / BG_BM + std::min(A.M, A.E) : (A.M + BG_BM - 1) / BG_BM;
+template <typename T, int BM> static void launch_big(const LinearI8Args &A, hipStream_t st) {
+  const int64_t tiles = A.offsets ? A.M / BM + std::min(A.M, A.E) : (A.M + BM - 1) / BM;
   const int64_t items = tiles * ((A.N + BG_BN - 1) / BG_BN);
   const unsigned grid = (unsigned)((items + 7) / 8 * 8);
-  if (A.E <= 64) linear_i8_big_kernel<T, 1><<<grid, 256, 0, st>>>(A);
-  else linear_i8_big_kernel<T, 16><<<grid, 256, 0, st>>>(A);
+  if (A.E <= 64) linear_i8_big_kernel<T, 1, BM><<<grid, 256, 0, st>>>(A);
+  else linear_i8_big_kernel<T, 16, BM><<<grid, 256, 0, st>>>(A);
 }
 
 template <typename T> static void launch_linear(const LinearI8Args &A, hipStream_t st) {
   const int avg = A.M / A.E;
   const bool near = (uint64_t)A.N * A.ldw < (1ull << 32) && (uint64_t)A.a_rows * A.lda < (1ull << 32);
-  if (avg > 64 && near) launch_big<T>(A, st);
+  // (tiles of 256 rows that the average says there are)
+  const int64_t tiles = (int64_t)ceil_div_h(avg, BG_BM) * A.E * ceil_div_h(A.N, BG_BN);
+  if (avg > 64 && near && tiles >= 256) launch_big<T, 256>(A, st);
+  else if (avg > 64 && near) launch_big<T, 64>(A, st);
   else if (avg <= 8) launch_short<T, 1, 4>(A, st);
   else if (avg <= 24) launch_short<T, 2, 4>(A, st);
   else launch_short<T, 4, 8>(A, st);

@@ -116,79 +116,63 @@ template <typename T> DEV void put4(T *p, bool vec, int n, int N, const float *v
   }
 }
 
-// ---- few rows per matrix: bound by reading the matrices once.
+// ---- small launches (one token's experts, a few rows by one matrix): bound by
+// latency, so every byte of the matrices is asked for at once.
 //
-// A block takes 16 MF rows (one tile of the list) and a range of output
-// channels in fragments of 16.  The rows go into LDS once, in the order in
-// which the matrix instructions read them (fragment m, step s of 64: 1 KB,
-// lane after lane; rows too long for that are read from memory each time).
-// The matrix goes straight into registers: a wave keeps the next D steps in
-// flight while it multiplies the current D, across fragments, without a
-// barrier.  KS = 1: every wave has fragments of its own.  KS = NW: the waves
-// share the fragments and split the steps (wave w takes steps w, w + NW, ..),
-// their sums are added through LDS; for launches with too few fragments to
-// give every wave one.
-template <typename T, int MF, int NW, int KS, int D, int NC, bool ALDS>
-__global__ __launch_bounds__(64 * NW) void linear_i8_short_kernel(LinearI8Args A, int per) {
-  constexpr int BM = 16 * MF, FW = NW / KS;
+// A block takes a tile of up to 16 rows and `per` fragments of 16 output
+// channels.  The rows go into LDS once, in the order in which the matrix
+// instructions read them (step s of 64: 1 KB, lane after lane; rows too long
+// for that are read from memory each time).  The four waves split the steps
+// (wave w takes steps w, w + 4, ..) and read the matrix straight into
+// registers, D steps ahead and across fragments; their sums are added
+// through LDS.
+constexpr int SH_BM = 16, SH_WAVES = 4;
+
+template <typename T, int D, int NC, bool ALDS>
+__global__ __launch_bounds__(64 * SH_WAVES) void linear_i8_short_kernel(LinearI8Args A, int per) {
+  constexpr int KS = SH_WAVES;
   extern __shared__ __attribute__((aligned(16))) int8_t lds_a[];
-  __shared__ __attribute__((aligned(16))) int red[KS > 1 ? KS * MF * 256 : 4];
+  __shared__ __attribute__((aligned(16))) int red[KS * 256];
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int fw = KS > 1 ? 0 : w, kw = KS > 1 ? w : 0;
   const int steps = (A.K + 63) >> 6, nfr = (A.N + 15) >> 4;
-  const int ns = (steps - kw + KS - 1) / KS, groups = (ns + D - 1) / D;
-  const int f0 = blockIdx.x * FW * per + fw;
-  const int cnt = max(0, min(per, (nfr - f0 + FW - 1) / FW));
+  const int ns = (steps - w + KS - 1) / KS, groups = (ns + D - 1) / D;
+  const int f0 = blockIdx.x * per, cnt = min(per, nfr - f0);
   const int ldw = (int)A.ldw;
   const bool vec = (((uintptr_t)A.out & (4 * sizeof(T) - 1)) | (A.ldo & 3)) == 0;
 
   RowTile R;
-  for (int t = blockIdx.y; TileList<BM, NC>(A.offsets, A.E, A.M).get(t, R); t += gridDim.y) {
+  for (int t = blockIdx.y; TileList<SH_BM, NC>(A.offsets, A.E, A.M).get(t, R); t += gridDim.y) {
     const int8_t *we = A.w + (size_t)R.e * A.N * A.ldw;
     // steps D g .. D g + D - 1 of this wave's fragment i (the last one again
     // behind the end: read twice, not used)
     uint4 ring[D];
-    auto column = [&](int i) {
-      return we + (size_t)min(16 * (f0 + FW * i) + lr, A.N - 1) * A.ldw;
-    };
-    auto at_step = [&](int s) { return min(64 * (kw + KS * min(s, ns - 1)) + 16 * lg, ldw - 16); };
-    if (cnt > 0 && ns > 0) {
+    auto column = [&](int i) { return we + (size_t)min(16 * (f0 + i) + lr, A.N - 1) * A.ldw; };
+    auto at_step = [&](int s) { return min(64 * (w + KS * min(s, ns - 1)) + 16 * lg, ldw - 16); };
+    if (ns > 0) {
       const int8_t *c = column(0);
 #pragma unroll
       for (int j = 0; j < D; ++j) ring[j] = ld16(c + at_step(j));
     }
-    int rows[MF];
-    float sa[MF];
-#pragma unroll
-    for (int m = 0; m < MF; ++m) {
-      rows[m] = source_row(A, min(R.p0 + 16 * m + lr, R.end - 1));
-      sa[m] = A.a_scale[rows[m]];
-    }
+    const int row = source_row(A, min(R.p0 + lr, R.end - 1));
+    const int8_t *ap = A.a + (size_t)row * A.lda + 16 * lg;
+    const float sa = A.a_scale[row];
     if constexpr (ALDS) {
       // (what stands in the places of rows behind the end reaches only those
       // rows' sums, which are not stored)
-      for (int s = w; s < steps; s += NW) {
-        uint4 v[MF];
-#pragma unroll
-        for (int m = 0; m < MF; ++m)
-          if (R.p0 + 16 * m + lr < R.end)
-            v[m] = ld16(A.a + (size_t)rows[m] * A.lda + 64 * s + 16 * lg);
-#pragma unroll
-        for (int m = 0; m < MF; ++m)
-          if (R.p0 + 16 * m + lr < R.end)
-            *reinterpret_cast<uint4 *>(lds_a + ((m * steps + s) * 64 + lane) * 16) = v[m];
-      }
+      for (int s = w; s < steps; s += KS)
+        if (R.p0 + lr < R.end)
+          *reinterpret_cast<uint4 *>(lds_a + (s * 64 + lane) * 16) = ld16(ap + 64 * s);
       __syncthreads();
     }
     for (int i = 0; i < cnt; ++i) {
       // the channels' scales, asked for before the next steps of the matrix
-      const int n = 16 * (f0 + FW * i) + 4 * lg;
+      const int n = 16 * (f0 + i) + 4 * lg;
       const float *ws = A.w_scale ? A.w_scale + (size_t)R.e * A.N : A.a_scale;
       float sw[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) sw[c] = ws[A.w_scale ? min(n + c, A.N - 1) : 0];
-      i32x4_t acc[MF] = {};
+      i32x4_t acc = {};
       auto group = [&](int g, auto prefetch) {
         constexpr bool PF = decltype(prefetch)::value;
         const bool wrap = g + 1 == groups;
@@ -198,16 +182,11 @@ __global__ __launch_bounds__(64 * NW) void linear_i8_short_kernel(LinearI8Args A
         for (int j = 0; j < D; ++j) {
           const int s = g * D + j;
           if (s < ns) {
-            const int sk = kw + KS * s;
-#pragma unroll
-            for (int m = 0; m < MF; ++m) {
-              uint4 av;
-              if constexpr (ALDS)
-                av = *reinterpret_cast<const uint4 *>(lds_a + ((m * steps + sk) * 64 + lane) * 16);
-              else
-                av = ld16(A.a + (size_t)rows[m] * A.lda + 64 * sk + 16 * lg);
-              acc[m] = mfma_i8(ring[j], av, acc[m]);
-            }
+            const int sk = w + KS * s;
+            uint4 av;
+            if constexpr (ALDS) av = *reinterpret_cast<const uint4 *>(lds_a + (sk * 64 + lane) * 16);
+            else av = ld16(ap + 64 * sk);
+            acc = mfma_i8(ring[j], av, acc);
           }
           if constexpr (PF) ring[j] = ld16(nc + at_step(ng * D + j));
         }
@@ -216,68 +195,45 @@ __global__ __launch_bounds__(64 * NW) void linear_i8_short_kernel(LinearI8Args A
         if (g + 1 < groups || i + 1 < cnt) group(g, std::true_type{});
         else group(g, std::false_type{});
       }
-      if constexpr (KS > 1) {
-        i32x4_t *rv = reinterpret_cast<i32x4_t *>(red);
+      i32x4_t *rv = reinterpret_cast<i32x4_t *>(red);
+      rv[w * 64 + lane] = acc;
+      __syncthreads();
+      if (w == 0) {
 #pragma unroll
-        for (int m = 0; m < MF; ++m) rv[(w * MF + m) * 64 + lane] = acc[m];
-        __syncthreads();
+        for (int o = 1; o < KS; ++o) acc += rv[o * 64 + lane];
+        const int p = R.p0 + lr;
+        if (p < R.end && n < A.N) {
+          float v[4];
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-          if (m % KS != w) continue;   // fragment m is added by wave m % KS
-#pragma unroll
-          for (int o = 1; o < KS; ++o) acc[m] += rv[(((w + o) % KS) * MF + m) * 64 + lane];
+          for (int c = 0; c < 4; ++c) v[c] = (float)acc[c] * (sa * (A.w_scale ? sw[c] : 1.0f));
+          put4<T>((T *)A.out + (size_t)p * A.ldo + n, vec, n, A.N, v);
         }
       }
-#pragma unroll
-      for (int m = 0; m < MF; ++m) {
-        if (KS > 1 && m % KS != w) continue;
-        const int p = R.p0 + 16 * m + lr;
-        if (p >= R.end || n >= A.N) continue;
-        float v[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = (float)acc[m][c] * (sa[m] * (A.w_scale ? sw[c] : 1.0f));
-        put4<T>((T *)A.out + (size_t)p * A.ldo + n, vec, n, A.N, v);
-      }
-      if constexpr (KS > 1) __syncthreads();   // the sums are read before the next ones are written
+      __syncthreads();   // the sums (and the rows) are read before the next ones are written
     }
-    if constexpr (ALDS) __syncthreads();       // and the rows before the next tile's
   }
 }
 
-// Short launches: rows per tile from the average rows of a matrix (each tile
-// reads its matrix once; more rows a tile cost LDS, fewer read the matrix
-// again), the waves' share from the number of fragments.
-template <typename T, int MF, int NW> static void launch_short(const LinearI8Args &A, hipStream_t st) {
-  constexpr int BM = 16 * MF;
-  const int steps = (A.K + 63) / 64, nfr = (A.N + 15) / 16;
-  // at most one tile more than M / BM per expert, and none without a row
-  const int tiles = A.offsets ? std::min(A.M, A.M / BM + A.E) : (A.M + BM - 1) / BM;
-  const size_t lds = (size_t)BM * steps * 64;
+// at most one tile more than M / 16 per expert, and none without a row
+static int short_tiles(const LinearI8Args &A) {
+  return A.offsets ? std::min(A.M, A.M / SH_BM + A.E) : (A.M + SH_BM - 1) / SH_BM;
+}
+
+template <typename T> static void launch_short(const LinearI8Args &A, hipStream_t st) {
+  const int steps = (A.K + 63) / 64, nfr = (A.N + 15) / 16, tiles = short_tiles(A);
+  const size_t lds = (size_t)SH_BM * steps * 64;
   const bool alds = lds <= 128 * 1024;
-  // enough waves to ask every CU for several blocks' worth of the matrix
-  const bool split = (int64_t)nfr * tiles < 4096;
-  const int ns = split ? (steps + NW - 1) / NW : steps;
-  const int per = split ? (nfr * tiles + 1023) / 1024 : (int)std::max<int64_t>(1, std::min<int64_t>(
-      nfr / NW, ((int64_t)nfr * tiles + NW * 1024 - 1) / (NW * 1024)));
-  dim3 grid(((nfr + per - 1) / per + (split ? 1 : NW) - 1) / (split ? 1 : NW), std::min(tiles, 32768));
-  // steps in flight: the depth that leaves the fewest empty places
-  const int pad8 = (ns + 7) / 8 * 8 - ns, pad12 = (ns + 11) / 12 * 12 - ns;
-  const int depth = ns <= 4 ? 4 : ns <= 8 ? 8 : pad12 < pad8 ? 12 : ns >= 16 && ns % 16 == 0 ? 16 : 8;
-#define MOE_L(KS, D, NC, AL) \
-  linear_i8_short_kernel<T, MF, NW, KS, D, NC, AL><<<grid, 64 * NW, AL ? lds : 0, st>>>(A, per)
-#define MOE_LE(KS, D)                            \
-  if (A.E <= 64) MOE_L(KS, D, 1, true);          \
-  else MOE_L(KS, D, 16, true);
-  if (!alds) {
-    if (split) MOE_L(NW, 8, 16, false);
-    else MOE_L(1, 8, 16, false);
-  } else if (split) {
-    if (ns <= 4) { MOE_LE(NW, 4) } else { MOE_LE(NW, 8) }
-  } else if (depth == 4) { MOE_LE(1, 4)
-  } else if (depth == 8) { MOE_LE(1, 8)
-  } else if (depth == 12) { MOE_LE(1, 12)
-  } else { MOE_LE(1, 16) }
-#undef MOE_LE
+  // about four blocks per CU: more of them pay for their set-up, fewer leave
+  // the memory system idle
+  const int per = (int)std::min<int64_t>(nfr, ((int64_t)nfr * tiles + 1023) / 1024);
+  const dim3 grid((nfr + per - 1) / per, std::min(tiles, 32768));
+#define MOE_L(D, NC, AL) \
+  linear_i8_short_kernel<T, D, NC, AL><<<grid, 64 * SH_WAVES, AL ? lds : 0, st>>>(A, per)
+  if (!alds) MOE_L(8, 16, false);
+  else if (A.E > 64 && steps <= 16) MOE_L(4, 16, true);
+  else if (A.E > 64) MOE_L(8, 16, true);
+  else if (steps <= 16) MOE_L(4, 1, true);
+  else MOE_L(8, 1, true);
 #undef MOE_L
 }
 
@@ -431,7 +387,7 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
 // share its L2.  The run is an eighth of the tiles there are, not of the grid.
 // BM: rows of a tile, 256 or, where those are too few to fill the chip, 64.
 template <typename T, int NC, int BM>
-__global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void linear_i8_big_kernel(LinearI8Args A) {
+__global__ __launch_bounds__(256, BM <= 64 ? 4 : 2) void linear_i8_big_kernel(LinearI8Args A) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[bg_lds(BM)];
   const int nt = (A.N + BG_BN - 1) / BG_BN;
   RowTile R;
@@ -446,7 +402,8 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void linear_i8_big_kernel(Li
     if (!list.get(t, R)) return;
   }
   const int rows = R.end - R.p0;
-  if (BM == 64 || rows <= 64) big_tile<T, 2>(A, R, n0, lds);
+  if constexpr (BM <= 64) big_tile<T, BM / 32>(A, R, n0, lds);
+  else if (rows <= 64) big_tile<T, 2>(A, R, n0, lds);
   else if (rows <= 128) big_tile<T, 4>(A, R, n0, lds);
   else if (rows <= 192) big_tile<T, 6>(A, R, n0, lds);
   else big_tile<T, 8>(A, R, n0, lds);
@@ -462,14 +419,15 @@ template <typename T, int BM> static void launch_big(const LinearI8Args &A, hipS
 
 template <typename T> static void launch_linear(const LinearI8Args &A, hipStream_t st) {
   const int avg = A.M / A.E;
+  // 32-bit byte offsets inside a and inside one matrix
   const bool near = (uint64_t)A.N * A.ldw < (1ull << 32) && (uint64_t)A.a_rows * A.lda < (1ull << 32);
+  const bool small = (int64_t)ceil_div_h(A.N, 16) * short_tiles(A) < 1024;
   // (tiles of 256 rows that the average says there are)
   const int64_t tiles = (int64_t)ceil_div_h(avg, BG_BM) * A.E * ceil_div_h(A.N, BG_BN);
-  if (avg > 64 && near && tiles >= 256) launch_big<T, 256>(A, st);
-  else if (avg > 64 && near) launch_big<T, 64>(A, st);
-  else if (avg <= 8) launch_short<T, 1, 4>(A, st);
-  else if (avg <= 24) launch_short<T, 2, 4>(A, st);
-  else launch_short<T, 4, 8>(A, st);
+  if (small || !near) launch_short<T>(A, st);
+  else if (avg <= 8) launch_big<T, 32>(A, st);
+  else if (avg <= 64 || tiles < 256) launch_big<T, 64>(A, st);
+  else launch_big<T, 256>(A, st);
 }
 
 void launch_linear_i8(bool bf16, const LinearI8Args &A, hipStream_t st) {

@@ -420,8 +420,8 @@ moe_status moe_adamw_step(const moe_adamw_hparams *h, int64_t n, float *master,
  *   logits    f32 [T][E], as moe_route writes them
  *   topk_idx  i32 [T][k]; an entry outside [0, E) is counted nowhere
  *   valid     u8 [T] or NULL (every token): 0 marks a token that takes no
- *             part.  Nothing of its row is read: its logits may hold anything,
- *             it is not counted, its row of dlogits is 0
+ *             part.  Nothing of its row counts: its logits and its topk_idx
+ *             may hold anything, its row of dlogits is 0
  *   loss      f32 [1] (out)
  *   counts    i32 [E+1] (out): slots per expert, then n
  *   prob      f32 [E] (out)
@@ -453,8 +453,8 @@ moe_status moe_balance_bwd(const moe_dims *dims, const float *logits, const floa
  *   dy          act [T][d], e_out act [S][d] (permuted order): 16-byte aligned
  *   topk_idx, gates, slot_pos  as written by moe_route and moe_permute
  *               (indices outside their range are clamped into it)
- *   valid       u8 [T] or NULL; the row of a token marked 0 is set to 0 and
- *               nothing of that token is read
+ *   valid       u8 [T] or NULL; the row of a token marked 0 is set to 0, and
+ *               whatever its rows of dy, e_out and dlogits_in hold
  *   dlogits_in  f32 [T][E] or NULL (0), e.g. from moe_balance_bwd
  *   dlogits     f32 [T][E] (out); may be dlogits_in */
 moe_status moe_gate_bwd(const moe_dims *dims, const void *dy, const void *e_out,
@@ -473,8 +473,8 @@ moe_status moe_gate_bwd(const moe_dims *dims, const void *dy, const void *e_out,
  * and sums keep float32 accuracy; dx is rounded to act once.
  *   x          act [T][d], 16-byte aligned; read only for dw_router
  *   w_router   f32 [d][E]; read only for dx
- *   valid      u8 [T] or NULL; a token marked 0 takes no part: its rows of x
- *              and dlogits are not read, its row of dx is that of dx_in (or 0)
+ *   valid      u8 [T] or NULL; a token marked 0 takes no part, whatever its rows
+ *              of x and dlogits hold: its row of dx is that of dx_in (or 0)
  *   dlogits    f32 [T][E]
  *   dx_in      act [T][d] or NULL (0), 16-byte aligned
  *   dx         act [T][d] (out) or NULL, 16-byte aligned; may be dx_in

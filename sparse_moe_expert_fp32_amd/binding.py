@@ -436,18 +436,21 @@ def moe_i8_linear(a, a_scale, w, w_scale, out, offsets=None, row_src=None, row_d
     f, dev, act = "moe_i8_linear", _gpu("moe_i8_linear", a), _act_code("moe_i8_linear", "out", out)
     R, Ka, lda = _rows(f, "a", a, _I8, dev)
     M, N, ldo = _rows(f, "out", out, out.dtype, dev)
-    if w.dim() != 3 or w.dtype not in (_I8, _U8) or w.get_device() != dev or w.shape[1] != N or \
-            (w.stride(2) != 1 and w.shape[2] > 1):
+    E, Nw, K = w.shape if w.dim() == 3 else (0, 0, 0)
+    es, ldw, one = w.stride() if E else (0, 0, 0)
+    if not E or Nw != N or (w.dtype is not _I8 and w.dtype is not _U8) or \
+            w.get_device() != dev or (one != 1 and K > 1):
         raise MoeError(f"{f}: w must be int8 [E][{N}][K] with adjacent columns on GPU {dev}, got "
                        f"{w.dtype} {tuple(w.shape)} {w.stride()} on {w.device}")
-    E, _, K = w.shape
-    es, ldw, _ = w.stride()
-    if N == 1:
-        ldw = es if E > 1 else max(ldw, K)
-    if E > 1 and es != N * ldw:
-        raise MoeError(f"{f}: the experts' matrices must lie one after another")
-    if w.untyped_storage().nbytes() - w.storage_offset() < E * N * ldw:
-        raise MoeError(f"{f}: the last row of w must reach its stride")
+    if K % 16 or not w.is_contiguous():
+        if N == 1:
+            ldw = es if E > 1 else max(ldw, K)
+        if E > 1 and es != N * ldw:
+            raise MoeError(f"{f}: the experts' matrices must lie one after another")
+        if w.untyped_storage().nbytes() - w.storage_offset() < E * N * ldw:
+            raise MoeError(f"{f}: the last row of w must reach its stride")
+    else:
+        ldw = K
     if Ka < moe_i8_stride(K):
         raise MoeError(f"{f}: a must have rows of at least {moe_i8_stride(K)} values")
     _call(f, dev, LIB.moe_i8_linear,

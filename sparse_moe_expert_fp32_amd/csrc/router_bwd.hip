@@ -19,6 +19,19 @@
 
 namespace moe {
 
+// The sum over the wave, in every lane: exchanges inside each row of 16 lanes
+// (pairs, quads, halves, rows), then the four row sums.
+DEV float wave_sum(float v) {
+#define MOE_DPP(C) __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), C, 0xF, 0xF, false))
+  v += MOE_DPP(0xB1);    // quad_perm [1, 0, 3, 2]
+  v += MOE_DPP(0x4E);    // quad_perm [2, 3, 0, 1]
+  v += MOE_DPP(0x141);   // row_half_mirror
+  v += MOE_DPP(0x140);   // row_mirror
+#undef MOE_DPP
+  auto row = [&](int r) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16 * r)); };
+  return (row(0) + row(1)) + (row(2) + row(3));
+}
+
 // 16 bytes of T as floats
 template <typename T> struct V16;
 template <> struct V16<float> {
@@ -86,16 +99,12 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(
     }
 #pragma unroll
     for (int j = 0; j < KM; ++j) {
-      float s = part[j];
-#pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
+      const float s = wave_sum(part[j]);
       if (lane == j0 + j) dgj = s;
     }
   }
   if (lane >= k) dgj = 0.f;
-  float mean = gj * dgj;
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) mean += __shfl_xor(mean, off);
+  const float mean = wave_sum(gj * dgj);
   const float dsel = gj * (dgj - mean);
   for (int e = lane; e < ((E + 63) & ~63); e += 64) {
     float v = dl_in && e < E ? dl_in[(size_t)t * E + e] : 0.f;

@@ -344,7 +344,9 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
     load(j + 1);
     __builtin_amdgcn_s_waitcnt(kWaitLds);
     block_barrier();
+    __builtin_amdgcn_s_setprio(1);
     multiply();
+    __builtin_amdgcn_s_setprio(0);
     block_barrier();
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -387,7 +389,7 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
 // share its L2.  The run is an eighth of the tiles there are, not of the grid.
 // BM: rows of a tile, 256 or, where those are too few to fill the chip, 64.
 template <typename T, int NC, int BM>
-__global__ __launch_bounds__(256, BM <= 64 ? 4 : 2) void linear_i8_big_kernel(LinearI8Args A) {
+__global__ __launch_bounds__(256, BM <= 64 ? 4 : BM == 128 ? 3 : 2) void linear_i8_big_kernel(LinearI8Args A) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[bg_lds(BM)];
   const int nt = (A.N + BG_BN - 1) / BG_BN;
   RowTile R;
@@ -404,6 +406,7 @@ __global__ __launch_bounds__(256, BM <= 64 ? 4 : 2) void linear_i8_big_kernel(Li
   const int rows = R.end - R.p0;
   if constexpr (BM <= 64) big_tile<T, BM / 32>(A, R, n0, lds);
   else if (rows <= 64) big_tile<T, 2>(A, R, n0, lds);
+  else if constexpr (BM == 128) big_tile<T, 4>(A, R, n0, lds);
   else if (rows <= 128) big_tile<T, 4>(A, R, n0, lds);
   else if (rows <= 192) big_tile<T, 6>(A, R, n0, lds);
   else big_tile<T, 8>(A, R, n0, lds);
@@ -427,6 +430,7 @@ template <typename T> static void launch_linear(const LinearI8Args &A, hipStream
   if (small || !near) launch_short<T>(A, st);
   else if (avg <= 8) launch_big<T, 32>(A, st);
   else if (avg <= 64 || tiles < 256) launch_big<T, 64>(A, st);
+  else if (avg <= 128) launch_big<T, 128>(A, st);
   else launch_big<T, 256>(A, st);
 }
 

@@ -281,20 +281,22 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     wo[i] = (uint32_t)min(n0 + tr + 32 * i, A.N - 1) * (uint32_t)A.ldw;
-  uint4 sa_[MI], sw_[4];   // the step on its way
-  auto load = [&](int s) {
-    const int k = BG_KS * min(s, steps - 1);
-    const uint32_t kw = (uint32_t)min(k + 16 * tc, (int)A.ldw - 16);
-    const int8_t *ak = A.a + k;
+  // The rows of the next step and the channels of the next two are on their
+  // way (the matrix comes from HBM, whose latency is longer than a step).
+  uint4 sa_[MI], w0[4], w1[4];
+  auto load_a = [&](int s) {
+    const uint32_t k = BG_KS * min(s, steps - 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sw_[i] = ld16(we + (size_t)(wo[i] + kw));
-#pragma unroll
-    for (int i = 0; i < MI; ++i) sa_[i] = ld16(ak + (size_t)ao[i]);
+    for (int i = 0; i < MI; ++i) sa_[i] = ld16(A.a + (size_t)(ao[i] + k));
   };
-  auto store = [&]() {
+  auto load_w = [&](uint4 (&v)[4], int s) {
+    const uint32_t k = (uint32_t)min(BG_KS * min(s, steps - 1) + 16 * tc, (int)A.ldw - 16);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint4 *>(lds + w_put + 32 * BG_KS * i) = sw_[i];
+    for (int i = 0; i < 4; ++i) v[i] = ld16(we + (size_t)(wo[i] + k));
+  };
+  auto store = [&](const uint4 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(lds + w_put + 32 * BG_KS * i) = v[i];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
       *reinterpret_cast<uint4 *>(lds + a_put + 32 * BG_KS * i) = sa_[i];
@@ -331,24 +333,34 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  load(0);
+  load_w(w0, 0);
+  load_a(0);
+  load_w(w1, 1);
   // the tile's scales wait in LDS for its end (the first barrier shows them)
   float *scales = reinterpret_cast<float *>(lds + BG_SCALES);
   scales[tid] = A.a_scale[source_row(A, min(R.p0 + tid, R.end - 1))];
   if (tid < BG_BN)
     scales[BG_BM + tid] =
         A.w_scale ? A.w_scale[(size_t)R.e * A.N + min(n0 + tid, A.N - 1)] : 1.0f;
-  for (int j = 0; j < steps; ++j) {
-    store();
+  auto step = [&](uint4 (&v)[4], int j) {
+    store(v);
     __builtin_amdgcn_sched_barrier(0);   // (the registers are free again)
-    load(j + 1);
+    load_a(j + 1);
+    __builtin_amdgcn_sched_barrier(0);   // (in this order: the rows are waited for first)
+    load_w(v, j + 2);
     __builtin_amdgcn_s_waitcnt(kWaitLds);
     block_barrier();
+    // (while this block multiplies, the other one of the CU should wait with
+    // its products, not the other way round: they then take turns)
     __builtin_amdgcn_s_setprio(1);
     multiply();
     __builtin_amdgcn_s_setprio(0);
     block_barrier();
     __builtin_amdgcn_sched_barrier(0);
+  };
+  for (int j = 0; j < steps; j += 2) {
+    step(w0, j);
+    if (j + 1 < steps) step(w1, j + 1);
   }
   const bool vec = (((uintptr_t)A.out & 15) | ((A.ldo * sizeof(T)) & 15)) == 0;
   f32x4_t sw[4];

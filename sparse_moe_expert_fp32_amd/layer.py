@@ -156,6 +156,10 @@ class DeviceLayer:
         for c in (B.CALL_BALANCE_FWD, B.CALL_ROUTER_BWD):
             self.ws[c] = torch.empty(max(1, B.moe_workspace_size(self.dm, c)), dtype=torch.uint8,
                                      device=self.dev)
+        # the router is its own float32 master
+        self.router_opt = {n: (torch.zeros_like(self.t[n]), torch.zeros_like(self.t[n]))
+                           for n in ("w_router", "b_router") if self.t.get(n) is not None}
+        self.router_step = 0
 
     def balance(self, valid=None, stream=None):
         """Load-balance loss and counts of the routed batch (after route())."""
@@ -176,6 +180,15 @@ class DeviceLayer:
                        valid, self.dlogits_bal, self.dlogits, stream)
         B.moe_router_bwd(self.dm, t["x"], t["w_router"], valid, self.dlogits, None, None,
                          self.dw_router, self.db_router, self.ws[B.CALL_ROUTER_BWD], stream)
+
+    def router_optimizer_step(self, lr=1e-4, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0,
+                              stream=None):
+        """One AdamW step on the router's weight and bias."""
+        self.router_step += 1
+        h = B.adamw_hparams(lr, beta1, beta2, eps, weight_decay, self.router_step)
+        for name, (m, v) in self.router_opt.items():
+            grad = self.dw_router if name == "w_router" else self.db_router
+            B.moe_adamw_step(h, self.t[name], grad, m, v, None, stream)
 
     def router_train_step(self, valid=None, stream=None):
         """train_step() with the load-balance loss and the router's gradients."""

@@ -56,6 +56,29 @@ def test_quant_rows(cuda_ok, M, K, dt):
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("K", [200, 768, 1027, 2048, 3001, 4096, 4100])
+def test_quant_many_rows(cuda_ok, K, dt):
+    """Row counts at which a wave takes a row; also by expert, and with rows
+    behind the last expert."""
+    M = 2100
+    x = torch.randn(M, K, generator=gen(K)).to(dt)
+    q, s = run_quant(x.to(DEV), K)
+    rq, rs = quant_ref(x.float())
+    assert torch.equal(s.cpu(), rs) and torch.equal(q.cpu()[:, :K], rq)
+    assert torch.all(q[:, K:] == 0)
+    E = 70
+    counts = torch.randint(0, 60, (E,), generator=gen(1))
+    off = torch.cat([torch.zeros(1), torch.cumsum(counts, 0).clamp(max=M - 3)]).to(torch.int32)
+    S = int(off[-1])
+    cs = torch.rand(E, K, generator=gen(2)) + 0.1
+    q, s = run_quant(x.to(DEV), K, col_scale=cs.to(DEV), offsets=off.to(DEV))
+    e = torch.searchsorted(off[1:].contiguous(), torch.arange(S, dtype=torch.int32), right=True)
+    rq, rs = quant_ref(x[:S].float() * cs[e])
+    assert torch.equal(s.cpu()[:S], rs) and torch.equal(q.cpu()[:S, :K], rq)
+    assert torch.all(q[S:] == 55) and torch.all(s[S:] == -77)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
 def test_quant_ties_and_extremes(cuda_ok, dt):
     """Quotients that end in one half go to the even side; zeros, subnormal
     and huge rows, and rows with values that are no numbers."""
@@ -116,7 +139,7 @@ def test_quant_channel_scales_by_expert(cuda_ok, K, dt):
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("M,K", [(1, 1), (4, 768), (37, 1001), (3, 5000)])
+@pytest.mark.parametrize("M,K", [(1, 1), (4, 768), (37, 1001), (3, 5000), (2050, 768), (2048, 130)])
 def test_quant_swiglu(cuda_ok, M, K, dt):
     gu = (torch.randn(M, 2 * K, generator=gen(M * K)) * 3).to(dt)
     gu[0, 0] = -200.0                                # exp(200) overflows: silu is 0
@@ -212,6 +235,36 @@ def test_linear_one_matrix(cuda_ok, M, N, K, dt):
 ])
 def test_linear_experts(cuda_ok, counts, N, K, div, dt):
     check_linear(counts, N, K, dt, seed=N + K, div=div)
+
+
+def spread(E, total, seed, odd=()):
+    """E row counts of about `total` in all: the given ones, empty ones, and
+    skewed ones."""
+    c = -torch.log1p(-torch.rand(E, generator=gen(seed)) * 0.999)
+    c = (c / c.sum() * total).int().tolist()
+    c[: len(odd)] = odd
+    c[len(odd)] = 0
+    return c
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,total,odd,N,K", [
+    (64, 300, (16, 17, 32, 33, 1), 1000, 200),                    # a few rows a matrix
+    (100, 500, (40,), 513, 1040),
+    (24, 700, (64, 65, 128, 129, 1), 700, 384),                   # tens of rows
+    (32, 2600, (64, 65, 128, 129, 256, 3), 1030, 272),            # about a hundred
+    (32, 6000, (64, 65, 128, 129, 192, 193, 256, 257, 600, 1), 1030, 160),   # hundreds
+    (40, 7000, (255, 31), 904, 129),
+])
+def test_linear_every_tile_height(cuda_ok, E, total, odd, N, K, dt):
+    check_linear(spread(E, total, E + K, list(odd)), N, K, dt, seed=E, div=3)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", [(3, 100, 6000), (17, 40, 8192), (5, 33, 8300), (20, 130, 4100),
+                                   (2100, 300, 5000), (1500, 2100, 70)])
+def test_linear_long_rows_and_many_rows(cuda_ok, M, N, K, dt):
+    check_linear([M], N, K, dt, seed=K, src=False)
 
 
 @pytest.mark.parametrize("kw", [

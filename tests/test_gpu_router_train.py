@@ -403,6 +403,43 @@ def test_router_training_on_a_side_stream_and_in_a_graph(cuda_ok):
         assert all(torch.equal(getattr(L, n), ref[n]) for n in RESULTS)
 
 
+def test_router_optimizer_step(cuda_ok):
+    """The router's own AdamW step moves w_router and b_router as the call on
+    copies of them does."""
+    cfg, L = layer(T=50, E=8, k=2)
+    L.router_train_step()
+    w, b = L.t["w_router"].clone(), L.t["b_router"].clone()
+    L.router_optimizer_step(lr=1e-2)
+    h = B.adamw_hparams(1e-2, 0.9, 0.95, 1e-8, 0.0, 1)
+    for master, g in ((w, L.dw_router), (b, L.db_router)):
+        m, v = torch.zeros_like(master), torch.zeros_like(master)
+        B.moe_adamw_step(h, master, g, m, v)
+    torch.cuda.synchronize()
+    assert torch.equal(L.t["w_router"], w) and torch.equal(L.t["b_router"], b)
+
+
+def test_two_layers_on_two_streams(cuda_ok):
+    """Each layer has its own workspaces: steps of two layers that overlap on
+    two streams give the bits that they give alone."""
+    a, b = layer(T=300, seed=1)[1], layer(T=900, E=40, seed=2)[1]
+    ref = []
+    for L in (a, b):
+        L.router_train_step()
+        torch.cuda.synchronize()
+        ref.append({n: getattr(L, n).clone() for n in RESULTS})
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        for L in (a, b):
+            for n in RESULTS:
+                getattr(L, n).fill_(-3)
+        torch.cuda.synchronize()
+        a.router_train_step(stream=sa)
+        b.router_train_step(stream=sb)
+        torch.cuda.synchronize()
+        for L, r in zip((a, b), ref):
+            assert all(torch.equal(getattr(L, n), r[n]) for n in RESULTS)
+
+
 def test_binding_refuses_wrong_tensors(cuda_ok):
     cfg, L = layer(T=20, E=8, k=2)
     L.forward()

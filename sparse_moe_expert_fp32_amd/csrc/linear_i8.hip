@@ -92,9 +92,23 @@ template <int BM, int NC> struct TileList {
   }
 };
 
-// The row of a that row p of the product reads (kept inside a).
+// The rows of a that the N rows p[..] of the product read (kept inside a).  The
+// lookups are all in flight at once: no load depends on a condition.
+template <int N> DEV void source_rows(const LinearI8Args &A, const int (&p)[N], int (&r)[N]) {
+  const int32_t *src = A.row_src ? A.row_src : reinterpret_cast<const int32_t *>(A.a_scale);
+  int raw[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) raw[i] = src[A.row_src ? p[i] : 0];
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    r[i] = min(max(A.row_src ? raw[i] / A.row_div : p[i], 0), A.a_rows - 1);
+}
 DEV int source_row(const LinearI8Args &A, int p) {
-  return min(max(A.row_src ? A.row_src[p] / A.row_div : p, 0), A.a_rows - 1);
+  const int q[1] = {p};
+  int r[1];
+  source_rows(A, q, r);
+  return r[0];
 }
 
 DEV uint4 ld16(const int8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
@@ -275,9 +289,13 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
   // byte offsets inside a and inside the matrix are below 2^32 (launch_linear)
   const int8_t *we = A.w + (size_t)R.e * A.N * A.ldw;
   uint32_t ao[MI], wo[4];
+  int rows[MI + 1], from[MI + 1];   // this thread's pieces, and the row whose scale it fetches
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
-    ao[i] = (uint32_t)source_row(A, min(R.p0 + tr + 32 * i, R.end - 1)) * (uint32_t)A.lda + 16 * tc;
+  for (int i = 0; i < MI; ++i) rows[i] = min(R.p0 + tr + 32 * i, R.end - 1);
+  rows[MI] = min(R.p0 + tid, R.end - 1);
+  source_rows(A, rows, from);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) ao[i] = (uint32_t)from[i] * (uint32_t)A.lda + 16 * tc;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     wo[i] = (uint32_t)min(n0 + tr + 32 * i, A.N - 1) * (uint32_t)A.ldw;
@@ -333,15 +351,19 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  load_w(w0, 0);
-  load_a(0);
-  load_w(w1, 1);
   // the tile's scales wait in LDS for its end (the first barrier shows them)
   float *scales = reinterpret_cast<float *>(lds + BG_SCALES);
-  scales[tid] = A.a_scale[source_row(A, min(R.p0 + tid, R.end - 1))];
-  if (tid < BG_BN)
-    scales[BG_BM + tid] =
-        A.w_scale ? A.w_scale[(size_t)R.e * A.N + min(n0 + tid, A.N - 1)] : 1.0f;
+  const float row_scale = A.a_scale[from[MI]];
+  const float col_scale = (A.w_scale ? A.w_scale + (size_t)R.e * A.N : A.a_scale)[
+      A.w_scale ? min(n0 + (tid & (BG_BN - 1)), A.N - 1) : 0];
+  __builtin_amdgcn_sched_barrier(0);   // (loads in this order: the first step waits for itself only)
+  load_w(w0, 0);
+  load_a(0);
+  __builtin_amdgcn_sched_barrier(0);
+  load_w(w1, 1);
+  __builtin_amdgcn_sched_barrier(0);
+  scales[tid] = row_scale;
+  if (tid < BG_BN) scales[BG_BM + tid] = A.w_scale ? col_scale : 1.0f;
   auto step = [&](uint4 (&v)[4], int j) {
     store(v);
     __builtin_amdgcn_sched_barrier(0);   // (the registers are free again)

@@ -356,10 +356,10 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
     A.template store<PA>(SA, slot);
     B.template store<PB>(SB, sb, KADJ ? nullptr : cs);
     __builtin_amdgcn_sched_barrier(0);
-    if (k + 2 * RB_KS < ke) {
-      A.load(SA, k + 2 * RB_KS);
-      B.load(SB, k + 2 * RB_KS);
-    }
+    // (behind the end too, from addresses inside: a load that may not happen
+    // would make the compiler wait for every load in flight)
+    A.load(SA, k + 2 * RB_KS);
+    B.load(SB, k + 2 * RB_KS);
     __builtin_amdgcn_s_waitcnt(0xC07F);   // (LDS only: the loads stay in flight)
     block_barrier();
     uint4 av[PA][4];
@@ -395,8 +395,10 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
   typename OB::Step b0, b1;
   A.load(a0, kb);
   B.load(b0, kb);
+  __builtin_amdgcn_sched_barrier(0);   // (in this order, so that the first step waits for itself only)
   A.load(a1, kb + RB_KS);
   B.load(b1, kb + RB_KS);
+  __builtin_amdgcn_sched_barrier(0);
   for (int k = kb; k < ke; k += 2 * RB_KS) {
     step(a0, b0, k, 0);
     if (k + RB_KS < ke) step(a1, b1, k + RB_KS, 1);

@@ -35,6 +35,8 @@
  *   - The layer calls keep no state between calls and are re-entrant.  The
  *     one exception is the instrumentation pair moe_timer_start/stop, which
  *     holds thread-local HIP events between its start and stop calls.
+ *   - A workspace belongs to one call at a time: calls that may overlap (other
+ *     streams, graphs that run side by side) take workspaces of their own.
  *   - Results are bitwise reproducible for identical inputs: integer
  *     histograms, scan-ordered placement, fixed-order reductions, no float
  *     atomics.
@@ -469,8 +471,10 @@ moe_status moe_gate_bwd(const moe_dims *dims, const void *dy, const void *e_out,
  * The dx of moe_adapter_bwd already holds the gates' share, so a training
  * step takes dx from the balance loss's gradient (dx_in = that dx) and the
  * weight gradients from the sum that moe_gate_bwd writes.  dw_router and
- * db_router have the router's layouts, ready for moe_adamw_step.  Products
- * and sums keep float32 accuracy; dx is rounded to act once.
+ * db_router have the router's layouts, ready for moe_adamw_step.  The weight
+ * and bias gradients, and dx in MOE_F32, keep float32 accuracy; for a dx in
+ * bf16 the operands of D W_r^T are taken to 16 bits, summed in float32 and the
+ * result is rounded once.
  *   x          act [T][d], 16-byte aligned; read only for dw_router
  *   w_router   f32 [d][E]; read only for dx
  *   valid      u8 [T] or NULL; a token marked 0 takes no part, whatever its rows

@@ -13,6 +13,12 @@
 // row for the backward; its column sums run in float32 per wave, then per
 // block in wave order, then over the blocks in double (the second kernel), so
 // the result does not depend on timing.
+//
+// Bound by the logits (65536 x 460: forward 35 us for 121 MB, its second
+// kernel 7 us, backward 39 us for 242 MB), at small sizes by the launches
+// (3 to 5 us a kernel).  The next token's row is on its way while one is
+// summed (55 -> 35 us), and the reductions over the lanes exchange registers
+// instead of going through LDS.
 #include <algorithm>
 
 #include "common.h"

@@ -4,6 +4,11 @@
 //   r = row_src ? row_src[p] / row_div : p,  offsets[e] <= p < offsets[e+1].
 // The sums are exact in int32 (K <= 65536); the two scales are applied in
 // float32 and the result is rounded once to the output type.
+//
+// Two kernels: a small launch asks for its matrices at once (short), any other
+// one runs row tiles of 32, 64, 128 or 256 through LDS (tiled).  The number of
+// rows of an expert is on the device only, so each block finds its tile from
+// the offsets itself: one launch per product, no list to build.
 #include <algorithm>
 #include <type_traits>
 
@@ -130,8 +135,9 @@ template <typename T> DEV void put4(T *p, bool vec, int n, int N, const float *v
   }
 }
 
-// ---- small launches (one token's experts, a few rows by one matrix): bound by
-// latency, so every byte of the matrices is asked for at once.
+// ---- the short kernel, for small launches (a few rows by one matrix): bound by
+// latency, so every byte of the matrices is asked for at once (8 us for 16 rows
+// by 2048 x 2048, most of it the launch).
 //
 // A block takes a tile of up to 16 rows and `per` fragments of 16 output
 // channels.  The rows go into LDS once, in the order in which the matrix
@@ -251,18 +257,32 @@ template <typename T> static void launch_short(const LinearI8Args &A, hipStream_
 #undef MOE_L
 }
 
-// ---- many rows per matrix: tiles of up to 256 rows x 128 channels, two
-// blocks of four waves per CU (2 x 2 waves, each half of the rows in
-// interleaved fragments of 16 and 64 channels), steps of 128 along K, so that
-// a row's share of a step is a whole 128-byte line.  A step goes from memory
-// into registers while the one before it is multiplied from LDS; one block of
-// the CU multiplies while the other one writes LDS or waits.  MI: 16-row
+// ---- the tiled kernel: tiles of up to BM rows x 128 channels, four waves per
+// block (2 x 2, each half of the rows in interleaved fragments of 16 and 64
+// channels), steps of 128 along K, so that a row's share of a step is a whole
+// 128-byte line (98304 rows by 460 matrices of 1536 x 2048: 658 us with half
+// lines, 604 with whole ones).
+//
+// A step goes from memory into registers and from there into one LDS slot; the
+// rows of the next step and the channels of the next two are on their way
+// while a step is multiplied, and nothing in the loop waits for more than it
+// needs (every load is unconditional and in the order of its use).  Two blocks
+// per CU at 256 rows (three at 128, four below) take turns: the one that
+// multiplies has priority, the other one writes LDS and waits (45 -> 41 us for
+// 8192 x 2048 x 2048).  256 x 256 tiles of eight waves with two LDS slots and
+// one block per CU were no faster (49 us where this then took 48).  MI: 16-row
 // fragments a wave has (32 MI rows); a tile runs as the smallest class that
 // holds its rows.
-constexpr int BG_BM = 256, BG_BN = 128, BG_KS = 128;
+//
+// What bounds it: a few rows a matrix, reading the matrices (64 matrices of
+// 1408 x 2048 in 27 us, 6.8 TB/s); hundreds of rows, the products (39 us for
+// 8192 x 2048 x 2048, 1.77 POP/s; 1.5 POP/s for 256 rows by each of 460
+// matrices of 1536 x 2048), whose instructions are issued a third of the time,
+// the rest going to LDS traffic and the two barriers of a step.
+constexpr int TL_BM = 256, TL_BN = 128, TL_KS = 128;
 // bytes of LDS for tiles of up to BM rows: channels, row and channel scales, rows
-constexpr int BG_SCALES = BG_BN * BG_KS, BG_A = BG_SCALES + (BG_BM + BG_BN) * 4;
-constexpr int bg_lds(int BM) { return BG_A + BM * BG_KS; }
+constexpr int TL_SCALES = TL_BN * TL_KS, TL_A = TL_SCALES + (TL_BM + TL_BN) * 4;
+constexpr int tl_lds(int BM) { return TL_A + BM * TL_KS; }
 
 // Rows of 128 bytes in LDS.  Chunk c (16 bytes) of row r stands at place
 // c ^ (r >> 1) & 7 for the rows of a, whose fragments read 16 adjacent rows,
@@ -270,22 +290,22 @@ constexpr int bg_lds(int BM) { return BG_A + BM * BG_KS; }
 // read the rows gt_col(f, 0..15): either way 16 lanes reading one chunk touch
 // every bank once.  The places are the same for every fragment of a wave and
 // every piece of a thread, so that all addresses are a base and a constant.
-DEV int bg_swz_a(int r) { return (r >> 1) & 7; }
-DEV int bg_swz_w(int r) { return ((r >> 2) & 6) | ((r >> 1) & 1); }
+DEV int tl_swz_a(int r) { return (r >> 1) & 7; }
+DEV int tl_swz_w(int r) { return ((r >> 2) & 6) | ((r >> 1) & 1); }
 
 constexpr int kWaitLds = 0xC07F;   // s_waitcnt lgkmcnt(0), nothing else
 
 template <typename T, int MI>
-DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds) {
+DEV void row_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds) {
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
   const int w = tid >> 6, wm = w & 1, wn = w >> 1;
   const int tr = tid >> 3, tc = tid & 7;     // row and chunk of this thread's first piece
-  const int steps = (A.K + BG_KS - 1) / BG_KS;   // (rows of a hold 0 behind K)
-  const int a_put = BG_A + tr * BG_KS + (tc ^ bg_swz_a(tr)) * 16;
-  const int w_put = tr * BG_KS + (tc ^ bg_swz_w(tr)) * 16;
+  const int steps = (A.K + TL_KS - 1) / TL_KS;   // (rows of a hold 0 behind K)
+  const int a_put = TL_A + tr * TL_KS + (tc ^ tl_swz_a(tr)) * 16;
+  const int w_put = tr * TL_KS + (tc ^ tl_swz_w(tr)) * 16;
   const int ar = 16 * wm + lr, wr = 64 * wn + gt_col(0, lr);
-  const int a_get = BG_A + ar * BG_KS + (lg ^ bg_swz_a(ar)) * 16;
-  const int w_get = wr * BG_KS + (lg ^ bg_swz_w(wr)) * 16;
+  const int a_get = TL_A + ar * TL_KS + (lg ^ tl_swz_a(ar)) * 16;
+  const int w_get = wr * TL_KS + (lg ^ tl_swz_w(wr)) * 16;
   // byte offsets inside a and inside the matrix are below 2^32 (launch_linear)
   const int8_t *we = A.w + (size_t)R.e * A.N * A.ldw;
   uint32_t ao[MI], wo[4];
@@ -303,21 +323,21 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
   // way (the matrix comes from HBM, whose latency is longer than a step).
   uint4 sa_[MI], w0[4], w1[4];
   auto load_a = [&](int s) {
-    const uint32_t k = BG_KS * min(s, steps - 1);
+    const uint32_t k = TL_KS * min(s, steps - 1);
 #pragma unroll
     for (int i = 0; i < MI; ++i) sa_[i] = ld16(A.a + (size_t)(ao[i] + k));
   };
   auto load_w = [&](uint4 (&v)[4], int s) {
-    const uint32_t k = (uint32_t)min(BG_KS * min(s, steps - 1) + 16 * tc, (int)A.ldw - 16);
+    const uint32_t k = (uint32_t)min(TL_KS * min(s, steps - 1) + 16 * tc, (int)A.ldw - 16);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = ld16(we + (size_t)(wo[i] + k));
   };
   auto store = [&](const uint4 (&v)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(lds + w_put + 32 * BG_KS * i) = v[i];
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(lds + w_put + 32 * TL_KS * i) = v[i];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
-      *reinterpret_cast<uint4 *>(lds + a_put + 32 * BG_KS * i) = sa_[i];
+      *reinterpret_cast<uint4 *>(lds + a_put + 32 * TL_KS * i) = sa_[i];
   };
   i32x4_t acc[MI][4] = {};
   // One step.  Row fragment q (half h = q / MI of the step, chunks 4 h + lg)
@@ -327,11 +347,11 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
   auto multiply = [&]() {
     uint4 wv[4], av[3];
     auto read_w = [&](int h, int f) {
-      wv[f] = *reinterpret_cast<const uint4 *>(lds + (w_get ^ (64 * h)) + BG_KS * gt_col(f, 0));
+      wv[f] = *reinterpret_cast<const uint4 *>(lds + (w_get ^ (64 * h)) + TL_KS * gt_col(f, 0));
     };
     auto read_a = [&](int q) {
       av[q % 3] = *reinterpret_cast<const uint4 *>(
-          lds + (a_get ^ (64 * (q / MI))) + 32 * BG_KS * (q % MI));
+          lds + (a_get ^ (64 * (q / MI))) + 32 * TL_KS * (q % MI));
     };
 #pragma unroll
     for (int f = 0; f < 4; ++f) read_w(0, f);
@@ -352,10 +372,10 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
     }
   };
   // the tile's scales wait in LDS for its end (the first barrier shows them)
-  float *scales = reinterpret_cast<float *>(lds + BG_SCALES);
+  float *scales = reinterpret_cast<float *>(lds + TL_SCALES);
   const float row_scale = A.a_scale[from[MI]];
   const float col_scale = (A.w_scale ? A.w_scale + (size_t)R.e * A.N : A.a_scale)[
-      A.w_scale ? min(n0 + (tid & (BG_BN - 1)), A.N - 1) : 0];
+      A.w_scale ? min(n0 + (tid & (TL_BN - 1)), A.N - 1) : 0];
   __builtin_amdgcn_sched_barrier(0);   // (loads in this order: the first step waits for itself only)
   load_w(w0, 0);
   load_a(0);
@@ -363,7 +383,7 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
   load_w(w1, 1);
   __builtin_amdgcn_sched_barrier(0);
   scales[tid] = row_scale;
-  if (tid < BG_BN) scales[BG_BM + tid] = A.w_scale ? col_scale : 1.0f;
+  if (tid < TL_BN) scales[TL_BM + tid] = A.w_scale ? col_scale : 1.0f;
   auto step = [&](uint4 (&v)[4], int j) {
     store(v);
     __builtin_amdgcn_sched_barrier(0);   // (the registers are free again)
@@ -388,7 +408,7 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
   f32x4_t sw[4];
 #pragma unroll
   for (int f = 0; f < 4; ++f)
-    sw[f] = *reinterpret_cast<const f32x4_t *>(scales + BG_BM + 64 * wn + gt_col(f, 4 * lg));
+    sw[f] = *reinterpret_cast<const f32x4_t *>(scales + TL_BM + 64 * wn + gt_col(f, 4 * lg));
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const int pl = 16 * (2 * i + wm) + lr, p = R.p0 + pl;
@@ -421,11 +441,11 @@ DEV void big_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
 // Blocks go round the 8 XCDs in turn; each XCD takes a contiguous run of the
 // (row tile, channel tile) list, so that tiles that share rows and matrices
 // share its L2.  The run is an eighth of the tiles there are, not of the grid.
-// BM: rows of a tile, 256 or, where those are too few to fill the chip, 64.
+// (Row tiles dealt out one by one to the XCDs: no difference.)
 template <typename T, int NC, int BM>
-__global__ __launch_bounds__(256, BM <= 64 ? 4 : BM == 128 ? 3 : 2) void linear_i8_big_kernel(LinearI8Args A) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[bg_lds(BM)];
-  const int nt = (A.N + BG_BN - 1) / BG_BN;
+__global__ __launch_bounds__(256, BM <= 64 ? 4 : BM == 128 ? 3 : 2) void linear_i8_tiled_kernel(LinearI8Args A) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[tl_lds(BM)];
+  const int nt = (A.N + TL_BN - 1) / TL_BN;
   RowTile R;
   int n0;
   {
@@ -434,38 +454,48 @@ __global__ __launch_bounds__(256, BM <= 64 ? 4 : BM == 128 ? 3 : 2) void linear_
     const int64_t at = blockIdx.x >> 3, item = run * (blockIdx.x & 7) + at;
     if (at >= run || item >= items) return;
     const int t = (int)(item / nt);
-    n0 = (int)(item - (int64_t)t * nt) * BG_BN;
+    n0 = (int)(item - (int64_t)t * nt) * TL_BN;
     if (!list.get(t, R)) return;
   }
   const int rows = R.end - R.p0;
-  if constexpr (BM <= 64) big_tile<T, BM / 32>(A, R, n0, lds);
-  else if (rows <= 64) big_tile<T, 2>(A, R, n0, lds);
-  else if constexpr (BM == 128) big_tile<T, 4>(A, R, n0, lds);
-  else if (rows <= 128) big_tile<T, 4>(A, R, n0, lds);
-  else if (rows <= 192) big_tile<T, 6>(A, R, n0, lds);
-  else big_tile<T, 8>(A, R, n0, lds);
+  if constexpr (BM <= 64) row_tile<T, BM / 32>(A, R, n0, lds);
+  else if (rows <= 64) row_tile<T, 2>(A, R, n0, lds);
+  else if constexpr (BM == 128) row_tile<T, 4>(A, R, n0, lds);
+  else if (rows <= 128) row_tile<T, 4>(A, R, n0, lds);
+  else if (rows <= 192) row_tile<T, 6>(A, R, n0, lds);
+  else row_tile<T, 8>(A, R, n0, lds);
 }
 
-template <typename T, int BM> static void launch_big(const LinearI8Args &A, hipStream_t st) {
+template <typename T, int BM> static void launch_tiled(const LinearI8Args &A, hipStream_t st) {
   const int64_t tiles = A.offsets ? A.M / BM + std::min(A.M, A.E) : (A.M + BM - 1) / BM;
-  const int64_t items = tiles * ((A.N + BG_BN - 1) / BG_BN);
+  const int64_t items = tiles * ((A.N + TL_BN - 1) / TL_BN);
   const unsigned grid = (unsigned)((items + 7) / 8 * 8);
-  if (A.E <= 64) linear_i8_big_kernel<T, 1, BM><<<grid, 256, 0, st>>>(A);
-  else linear_i8_big_kernel<T, 16, BM><<<grid, 256, 0, st>>>(A);
+  if (A.E <= 64) linear_i8_tiled_kernel<T, 1, BM><<<grid, 256, 0, st>>>(A);
+  else linear_i8_tiled_kernel<T, 16, BM><<<grid, 256, 0, st>>>(A);
 }
 
+// Which kernel, from the rows a matrix has on average (the host knows no more):
+//  - short where there are few fragments of 16 channels by 16 rows: 8.2 us
+//    against 9.4 for 16 rows by 2048 x 2048, 13.6 against 11.5 for 12 rows of
+//    12 experts (1152 fragments);
+//  - 32-row tiles up to 8 rows a matrix (259 us against 265 at 8 rows by 460
+//    matrices of 1536 x 2048, 124 against 137 at 1 row by 768 x 2048), 64-row
+//    tiles up to 64 (320 against 351 with 128-row tiles at 80), 128-row tiles
+//    up to 128 (373 against 383 with 256-row ones; at 160 448 against 412);
+//  - 64-row tiles also where 256-row ones are too few to fill the chip (777 x
+//    1001 x 1111: 12 us against 27).
 template <typename T> static void launch_linear(const LinearI8Args &A, hipStream_t st) {
   const int avg = A.M / A.E;
   // 32-bit byte offsets inside a and inside one matrix
   const bool near = (uint64_t)A.N * A.ldw < (1ull << 32) && (uint64_t)A.a_rows * A.lda < (1ull << 32);
   const bool small = (int64_t)ceil_div_h(A.N, 16) * short_tiles(A) < 1024;
   // (tiles of 256 rows that the average says there are)
-  const int64_t tiles = (int64_t)ceil_div_h(avg, BG_BM) * A.E * ceil_div_h(A.N, BG_BN);
+  const int64_t tiles = (int64_t)ceil_div_h(avg, TL_BM) * A.E * ceil_div_h(A.N, TL_BN);
   if (small || !near) launch_short<T>(A, st);
-  else if (avg <= 8) launch_big<T, 32>(A, st);
-  else if (avg <= 64 || tiles < 256) launch_big<T, 64>(A, st);
-  else if (avg <= 128) launch_big<T, 128>(A, st);
-  else launch_big<T, 256>(A, st);
+  else if (avg <= 8) launch_tiled<T, 32>(A, st);
+  else if (avg <= 64 || tiles < 256) launch_tiled<T, 64>(A, st);
+  else if (avg <= 128) launch_tiled<T, 128>(A, st);
+  else launch_tiled<T, 256>(A, st);
 }
 
 void launch_linear_i8(bool bf16, const LinearI8Args &A, hipStream_t st) {

@@ -13,7 +13,8 @@
 // adjacent columns a thread and chunk.  The first NH chunks stay in registers
 // between the maximum and the quantization (their index is a compile-time
 // constant: an index that a loop runs past the array would move other
-// registers); what lies behind them is computed again.
+// registers); what lies behind them is computed again.  Bound by memory:
+// 98304 x 768 SwiGLU rows in 93 us (378 MB), 8192 x 2048 in 15 us (50 MB).
 #include <algorithm>
 
 #include "common.h"
@@ -153,8 +154,8 @@ __global__ __launch_bounds__(256) void quant_i8_kernel(QuantArgs A) {
   }
 }
 
-// A wave per row up to 4096 columns when the rows fill the chip; a block of
-// four waves per row otherwise.
+// A wave per row up to 4096 columns when the rows fill the chip (eight waves a
+// CU from 2048 rows on); a block of four waves per row otherwise.
 constexpr int QU_WAVE_ROWS = 2048;
 
 template <typename T, bool VEC, bool SWIGLU>

@@ -7,10 +7,14 @@
 //   dsel_j   = g_j (dgamma_j - sum_i g_i dgamma_i),
 //   dlogits[t][e] = dlogits_in[t][e] + sum_{j: e_j = e} dsel_j.
 // One wave per token, the k dot products in groups of KM whose loads are in
-// flight together; bound by reading e_out once.
+// flight together; bound by reading e_out once (8192 tokens, k = 12, d = 2048:
+// 110 us for 470 MB).
 //
 // router_bwd, with D = dlogits:
 //   dx = dx_in + D W^T,  dW[c][e] = sum_t x[t][c] D[t][e],  db[e] = sum_t D[t][e].
+// Bound by the products (8192 x 2048 x 460 in three planes: dx 77 us, dW 77 us
+// and 7 for its partial sums, 0.6 PFLOP/s each; in float32 on the vector units
+// 1.3 ms each).
 #include <algorithm>
 
 #include "common.h"
@@ -146,11 +150,12 @@ void launch_gate_bwd(bool bf16, const void *dy, const void *e_out, const int32_t
 // one rounded: 2^-16).  Three matrix instructions of 16 clocks in the place of
 // the eight of 32 that float32 operands take (v_mfma_f32_16x16x4_f32).
 //
-// 128 x BN tile per block of four waves (2 x 2), steps of 32 along k through
-// two LDS slots; a step's values are loaded while the one before it is
-// multiplied and split into planes on their way into LDS.  An operand lies
-// with k adjacent (KADJ: rows of k) or with k as its row index (a thread then
-// takes eight rows of one column; neighbouring threads neighbouring columns).
+// 128 x BN tile per block of four waves (2 x 2), two blocks per CU, steps of 32
+// along k through two LDS slots; two steps are on their way while one is
+// multiplied, and are split into planes as they go into LDS (vector work of one
+// block beside the products of the other).  An operand lies with k adjacent
+// (KADJ: rows of k) or with k as its row index (a thread then takes eight rows
+// of one column; neighbouring threads neighbouring columns).
 constexpr int RB_BM = 128, RB_KS = 32;
 
 // An operand in LDS: planes of 64-byte rows.  Chunk c (16 bytes) of row r

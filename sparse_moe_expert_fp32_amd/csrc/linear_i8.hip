@@ -306,7 +306,10 @@ DEV void row_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
   const int ar = 16 * wm + lr, wr = 64 * wn + gt_col(0, lr);
   const int a_get = TL_A + ar * TL_KS + (lg ^ tl_swz_a(ar)) * 16;
   const int w_get = wr * TL_KS + (lg ^ tl_swz_w(wr)) * 16;
-  // byte offsets inside a and inside the matrix are below 2^32 (launch_linear)
+  // byte offsets inside the matrix, and inside a (from the tile's first row
+  // on, where the rows are not looked up), are below 2^32 (launch_linear)
+  const int first = A.row_src ? 0 : R.p0;
+  const int8_t *ab = A.a + (size_t)first * A.lda;
   const int8_t *we = A.w + (size_t)R.e * A.N * A.ldw;
   uint32_t ao[MI], wo[4];
   int rows[MI + 1], from[MI + 1];   // this thread's pieces, and the row whose scale it fetches
@@ -315,7 +318,7 @@ DEV void row_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
   rows[MI] = min(R.p0 + tid, R.end - 1);
   source_rows(A, rows, from);
 #pragma unroll
-  for (int i = 0; i < MI; ++i) ao[i] = (uint32_t)from[i] * (uint32_t)A.lda + 16 * tc;
+  for (int i = 0; i < MI; ++i) ao[i] = (uint32_t)(from[i] - first) * (uint32_t)A.lda + 16 * tc;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     wo[i] = (uint32_t)min(n0 + tr + 32 * i, A.N - 1) * (uint32_t)A.ldw;
@@ -325,7 +328,7 @@ DEV void row_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
   auto load_a = [&](int s) {
     const uint32_t k = TL_KS * min(s, steps - 1);
 #pragma unroll
-    for (int i = 0; i < MI; ++i) sa_[i] = ld16(A.a + (size_t)(ao[i] + k));
+    for (int i = 0; i < MI; ++i) sa_[i] = ld16(ab + (size_t)(ao[i] + k));
   };
   auto load_w = [&](uint4 (&v)[4], int s) {
     const uint32_t k = (uint32_t)min(TL_KS * min(s, steps - 1) + 16 * tc, (int)A.ldw - 16);
@@ -458,12 +461,19 @@ __global__ __launch_bounds__(256, BM <= 64 ? 4 : BM == 128 ? 3 : 2) void linear_
     if (!list.get(t, R)) return;
   }
   const int rows = R.end - R.p0;
-  if constexpr (BM <= 64) row_tile<T, BM / 32>(A, R, n0, lds);
-  else if (rows <= 64) row_tile<T, 2>(A, R, n0, lds);
-  else if constexpr (BM == 128) row_tile<T, 4>(A, R, n0, lds);
-  else if (rows <= 128) row_tile<T, 4>(A, R, n0, lds);
-  else if (rows <= 192) row_tile<T, 6>(A, R, n0, lds);
-  else row_tile<T, 8>(A, R, n0, lds);
+  if constexpr (BM <= 64) {
+    row_tile<T, BM / 32>(A, R, n0, lds);
+  } else {
+    if (rows <= 32) row_tile<T, 1>(A, R, n0, lds);
+    else if (rows <= 64) row_tile<T, 2>(A, R, n0, lds);
+    else if (rows <= 96) row_tile<T, 3>(A, R, n0, lds);
+    else if constexpr (BM == 128) row_tile<T, 4>(A, R, n0, lds);
+    else if (rows <= 128) row_tile<T, 4>(A, R, n0, lds);
+    else if (rows <= 160) row_tile<T, 5>(A, R, n0, lds);
+    else if (rows <= 192) row_tile<T, 6>(A, R, n0, lds);
+    else if (rows <= 224) row_tile<T, 7>(A, R, n0, lds);
+    else row_tile<T, 8>(A, R, n0, lds);
+  }
 }
 
 template <typename T, int BM> static void launch_tiled(const LinearI8Args &A, hipStream_t st) {
@@ -486,8 +496,9 @@ template <typename T, int BM> static void launch_tiled(const LinearI8Args &A, hi
 //    1001 x 1111: 12 us against 27).
 template <typename T> static void launch_linear(const LinearI8Args &A, hipStream_t st) {
   const int avg = A.M / A.E;
-  // 32-bit byte offsets inside a and inside one matrix
-  const bool near = (uint64_t)A.N * A.ldw < (1ull << 32) && (uint64_t)A.a_rows * A.lda < (1ull << 32);
+  // 32-bit byte offsets inside one matrix, and inside a where rows are looked up
+  const bool near = (uint64_t)A.N * A.ldw < (1ull << 32) &&
+                    (!A.row_src || (uint64_t)A.a_rows * A.lda < (1ull << 32));
   const bool small = (int64_t)ceil_div_h(A.N, 16) * short_tiles(A) < 1024;
   // (tiles of 256 rows that the average says there are)
   const int64_t tiles = (int64_t)ceil_div_h(avg, TL_BM) * A.E * ceil_div_h(A.N, TL_BN);

@@ -247,19 +247,28 @@ class Int8Experts:
         return (torch.empty(M, B.moe_i8_stride(K), dtype=torch.int8, device=dev),
                 torch.empty(M, dtype=torch.float32, device=dev))
 
-    def forward(self, L: DeviceLayer, stream=None):
-        """e_out of a routed and permuted layer L from its x."""
-        T, S, f = L.cfg.T, L.cfg.S, self.f
+    @staticmethod
+    def _on(stream):
+        """The buffers belong to the stream that the kernels run on."""
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
             raise TypeError("stream must be a torch.cuda.Stream or None")
-        with torch.cuda.stream(stream):
+        return torch.cuda.stream(stream)
+
+    def forward(self, L: DeviceLayer, stream=None):
+        """e_out of a routed and permuted layer L from its x."""
+        f2 = self.gate_up.shape[1]
+        shapes = [tuple(t.shape) for t in (self.gate_up, self.s_gate_up, self.down, self.s_down)]
+        if f2 % 2 or shapes[1:] != [(self.E, f2), (self.E, self.d, self.f), (self.E, self.d)]:
+            raise ValueError(f"Int8Experts: the shapes {shapes} do not match")
+        T, S, f = L.cfg.T, L.cfg.S, self.f
+        with self._on(stream):
             q, s = self._rows(T, self.d)
             gu = torch.empty(S, 2 * f, dtype=L.e_out.dtype, device=L.e_out.device)
             hq, hs = self._rows(S, f)
             B.moe_quant_i8(L.t["x"], q, s)
             B.moe_i8_linear(q, s, self.gate_up, self.s_gate_up, gu, offsets=L.offsets,
                             row_src=L.perm_src, row_div=L.cfg.k)
-            B.moe_quant_i8(gu[:, :f], hq, hs, mul=gu[:, f:])
+            B.moe_quant_i8(gu[:, :f], hq, hs, mul=gu[:, f:], offsets=L.offsets)
             B.moe_i8_linear(hq, hs, self.down, self.s_down, L.e_out, offsets=L.offsets)
         return gu
 
@@ -279,7 +288,7 @@ class Int8Experts:
         if self.t is None:
             self.transpose()
         w, cs = self.t[which], self.s_gate_up if which == "gate_up" else self.s_down
-        with torch.cuda.stream(stream):
+        with self._on(stream):
             q, s = self._rows(*dout.shape)
             dx = torch.empty(dout.shape[0], w.shape[1], dtype=dout.dtype, device=dout.device)
             B.moe_quant_i8(dout, q, s, col_scale=cs, offsets=offsets)

@@ -110,6 +110,26 @@ def test_quant_ties_and_extremes(cuda_ok, dt):
         assert torch.isnan(s[i]) and torch.all(q[i] == 0)
 
 
+@pytest.mark.parametrize("M", [40, 2100])
+def test_quant_next_to_a_half(cuda_ok, M):
+    """Quotients a few float32 steps to either side of n + 1/2, and on it, in
+    the first columns, in the middle of a row and in its last chunk."""
+    K = 1500
+    g = gen(M)
+    top = (torch.rand(M, 1, generator=g) + 0.5) * 2.0 ** torch.randint(-40, 40, (M, 1), generator=g)
+    s = (top.double() / 127).float()
+    half = torch.randint(-127, 127, (M, K), generator=g).double() + 0.5
+    v = (half * s.double()).float()
+    step = torch.randint(-3, 4, (M, K), generator=g)
+    v = (v.view(torch.int32) + step.to(torch.int32)).view(torch.float32)
+    v[:, 700:1490] = torch.randn(M, 790, generator=g) * top / 8   # (most chunks are ordinary)
+    v = torch.minimum(torch.maximum(v, -top), top)
+    v[:, 9] = top[:, 0]
+    q, sc = run_quant(v.to(DEV), K)
+    rq, rs = quant_ref(v)
+    assert torch.equal(sc.cpu(), rs) and torch.equal(q.cpu()[:, :K], rq)
+
+
 def test_quant_strides_and_wider_rows(cuda_ok):
     """Rows of a wider matrix off a 16-byte boundary, and q wider than needed."""
     for off in (0, 1, 8):
@@ -331,6 +351,26 @@ def test_linear_matrices_past_32_bits(cuda_ok, short):
         i, j = int(off[e]), int(off[e + 1])
         ref = (a[i:j].to(DEV).double() @ w[e].double().t()) * a_s[i:j].to(DEV).double()[:, None]
         assert torch.all((out[i:j].double() - ref).abs() <= ref.abs() * 3.1 * U)
+
+
+@pytest.mark.parametrize("looked_up", [False, True])
+def test_linear_rows_past_32_bits(cuda_ok, looked_up):
+    """2097452 rows of 2 KiB: the last ones lie behind 2^32 bytes."""
+    R, N, K = 2097152 + 300, 32, 2048
+    at = torch.tensor([0, 5, 255, 256, 2097151, 2097152, R - 257, R - 1])
+    a = torch.zeros(R, K, dtype=torch.int8, device=DEV)
+    vals = torch.randint(-127, 128, (len(at), K), generator=gen(1)).to(torch.int8).to(DEV)
+    a[at.to(DEV)] = vals
+    a_s = torch.rand(R, device=DEV)
+    w = torch.randint(-128, 128, (1, N, K), generator=gen(2)).to(torch.int8).to(DEV)
+    out = torch.empty(len(at) if looked_up else R, N, device=DEV)
+    B.moe_i8_linear(a, a_s, w, None, out,
+                    row_src=at.to(torch.int32).to(DEV) if looked_up else None)
+    got = out if looked_up else out[at.to(DEV)]
+    ref = (vals.double() @ w[0].double().t()) * a_s[at.to(DEV)].double()[:, None]
+    assert torch.all((got.double() - ref).abs() <= ref.abs() * 3.1 * U)
+    if not looked_up:
+        assert int((out != 0).any(1).sum()) == len(at)   # (the other rows are 0)
 
 
 def test_row_sources_out_of_range_are_clamped(cuda_ok):

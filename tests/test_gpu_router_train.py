@@ -122,6 +122,34 @@ def test_balance_without_a_token(cuda_ok):
     check_balance(l * float("inf"), idx, torch.zeros(9, dtype=torch.bool))
 
 
+@pytest.mark.parametrize("T,cut,E,k", [(300, 7, 40, 3), (513, 256, 460, 12)])
+def test_balance_counts_added_over_two_halves(cuda_ok, T, cut, E, k):
+    """A batch in two parts whose counts are added between the two calls: the
+    gradient has the whole batch's loads."""
+    l, idx, _ = route(T, E, k, T)
+    valid = torch.rand(T, generator=gen(1)) > 0.2
+    whole = balance_gpu(l, idx, valid, 0.5)
+    dl = torch.tensor([0.5], device=DEV)
+    parts = []
+    for s in (slice(0, cut), slice(cut, T)):
+        n = s.stop - s.start
+        dm = dims(n, 32, E, k)
+        new = lambda *n_, dt=torch.float32: torch.full(n_, -77, dtype=dt, device=DEV)  # noqa: E731
+        ld, v = l[s].to(DEV), valid[s].to(DEV)
+        loss, counts, prob, stats = new(1), new(E + 1, dt=torch.int32), new(E), new(n, 2)
+        ws = new(max(1, B.moe_workspace_size(dm, B.CALL_BALANCE_FWD)), dt=torch.int8)
+        B.moe_balance_fwd(dm, ld, idx[s].to(DEV), v, loss, counts, prob, stats, ws)
+        parts.append((dm, ld, v, stats, counts))
+    total = parts[0][4] + parts[1][4]
+    assert torch.equal(total, whole[1])
+    outs = []
+    for dm, ld, v, stats, _ in parts:
+        out = torch.empty_like(ld)
+        B.moe_balance_bwd(dm, ld, stats, total, v, dl, out)
+        outs.append(out)
+    assert torch.equal(torch.cat(outs), whole[4])   # (a row's arithmetic is the same)
+
+
 def test_balance_masked_experts_and_empty_rows(cuda_ok):
     """-inf logits have probability 0, a row of them adds nothing; the type's
     lowest value is a finite logit like others; same index twice, and indices

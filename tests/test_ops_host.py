@@ -126,3 +126,18 @@ def test_binding_refuses_tensors_off_the_gpu():
     with pytest.raises(B.MoeError, match="GPU"):
         B.moe_balance_bwd(B.dims(4, 128, 8, 2, 256, 4, 32, "f32"), z(4, 8), z(4, 2),
                           z(9, dtype=torch.int32), None, z(1), z(4, 8))
+
+
+@pytest.mark.parametrize("gu,s_gu,down,s_down", [
+    ((2, 7, 8), (2, 7), (2, 8, 3), (2, 8)),       # an odd number of gate/up channels
+    ((2, 8, 8), (2, 8), (2, 8, 5), (2, 8)),       # down reads another width
+    ((2, 8, 8), (2, 8), (3, 8, 4), (3, 8)),       # another number of experts
+    ((2, 8, 8), (2, 4), (2, 8, 4), (2, 8)),       # scales of gate only
+    ((2, 8, 8), (2, 8), (2, 8, 4), (2, 4)),
+])
+def test_int8_experts_refuse_shapes_that_do_not_match(gu, s_gu, down, s_down):
+    from sparse_moe_expert_fp32_amd.layer import Int8Experts
+    X = Int8Experts(torch.zeros(gu, dtype=torch.int8), torch.zeros(s_gu),
+                    torch.zeros(down, dtype=torch.int8), torch.zeros(s_down))
+    with pytest.raises(ValueError, match="Int8Experts"):
+        X.forward(None)

@@ -272,7 +272,8 @@ template <typename T> static void launch_short(const LinearI8Args &A, hipStream_
 // 8192 x 2048 x 2048).  256 x 256 tiles of eight waves with two LDS slots and
 // one block per CU were no faster (49 us where this then took 48).  MI: 16-row
 // fragments a wave has (32 MI rows); a tile runs as the smallest class that
-// holds its rows.
+// holds its rows (548 -> 532 us for 98304 uneven rows by 460 matrices of 1536 x
+// 2048 where the classes went in steps of 64 rows).
 //
 // What bounds it: a few rows a matrix, reading the matrices (64 matrices of
 // 1408 x 2048 in 27 us, 6.8 TB/s); hundreds of rows, the products (39 us for
@@ -488,29 +489,39 @@ template <typename T, int BM> static void launch_tiled(const LinearI8Args &A, hi
   else linear_i8_tiled_kernel<T, 16, BM><<<grid, 256, 0, st>>>(A);
 }
 
-// Which kernel, from the rows a matrix has on average (the host knows no more):
+// Which kernel, from the rows a matrix has on average (the host knows no more)
+// and the work in tiles of 128 x 128 (times of uneven loads, log-normal with
+// sigma 0.8):
 //  - short where there are few fragments of 16 channels by 16 rows: 8.2 us
 //    against 9.4 for 16 rows by 2048 x 2048, 13.6 against 11.5 for 12 rows of
 //    12 experts (1152 fragments);
-//  - 32-row tiles up to 8 rows a matrix (259 us against 265 at 8 rows by 460
-//    matrices of 1536 x 2048, 124 against 137 at 1 row by 768 x 2048), 64-row
-//    tiles up to 64 (320 against 351 with 128-row tiles at 80), 128-row tiles
-//    up to 128 (373 against 383 with 256-row ones; at 160 448 against 412);
-//  - 64-row tiles also where 256-row ones are too few to fill the chip (777 x
-//    1001 x 1111: 12 us against 27).
+//  - 32-row tiles up to 8 rows a matrix: 124 us against 137 at 1 row by 460
+//    matrices of 768 x 2048, 250 against 251 at 8 rows by 1536 x 2048, 267
+//    against 265 at 12;
+//  - 128-row tiles from three blocks a CU on, from one where they are full
+//    (256 rows a matrix): against 64-row ones 62 us for 64 at 64 rows by 128
+//    matrices of 2048 x 1024, 46 for 45 at 128 rows by 64 of 1408 x 2048; 19.5
+//    for 21.0 at 256 rows by 8 of 2048 x 2048, 15.6 for 15.4 at 160;
+//  - 256-row tiles where there is work for many rounds of them: 146 us against
+//    155 with 128-row ones at 600 rows by 64 matrices of 1408 x 2048, 104
+//    against 101 at 384 (102 against 106 with even loads), 62 against 57 at 213;
+//    422 against 439 at 160 rows by 460 of 1536 x 2048, 350 against 343 at 80.  With one matrix every tile is whole, and a round of
+//    them (two per CU) is enough: 39 us against 44 for 8192 rows by 2048 x 2048,
+//    25.7 against 22.9 for 4096.
 template <typename T> static void launch_linear(const LinearI8Args &A, hipStream_t st) {
   const int avg = A.M / A.E;
   // 32-bit byte offsets inside one matrix, and inside a where rows are looked up
   const bool near = (uint64_t)A.N * A.ldw < (1ull << 32) &&
                     (!A.row_src || (uint64_t)A.a_rows * A.lda < (1ull << 32));
   const bool small = (int64_t)ceil_div_h(A.N, 16) * short_tiles(A) < 1024;
-  // (tiles of 256 rows that the average says there are)
-  const int64_t tiles = (int64_t)ceil_div_h(avg, TL_BM) * A.E * ceil_div_h(A.N, TL_BN);
+  const int64_t work = (int64_t)A.M * A.N / (128 * 128);
+  const bool many = A.E == 1 ? (int64_t)ceil_div_h(A.M, TL_BM) * ceil_div_h(A.N, TL_BN) >= 512
+                             : avg > 112 && work >= 2000;
   if (small || !near) launch_short<T>(A, st);
   else if (avg <= 8) launch_tiled<T, 32>(A, st);
-  else if (avg <= 64 || tiles < 256) launch_tiled<T, 64>(A, st);
-  else if (avg <= 128) launch_tiled<T, 128>(A, st);
-  else launch_tiled<T, 256>(A, st);
+  else if (many) launch_tiled<T, 256>(A, st);
+  else if (work >= 768 || (avg >= 256 && work >= 256)) launch_tiled<T, 128>(A, st);
+  else launch_tiled<T, 64>(A, st);
 }
 
 void launch_linear_i8(bool bf16, const LinearI8Args &A, hipStream_t st) {

@@ -18,8 +18,10 @@
 // between the maximum and the quantization (their index is a compile-time
 // constant: an index that a loop runs past the array would move other
 // registers); what lies behind them, or is done again, is computed again.
-// Bound by memory at @FIG@; few rows by the latency of one pass, so that the
-// code on its way is kept short (a cold kernel waits for its instructions).
+// Bound by memory where there are many rows: 98304 x 768 SwiGLU rows in 69 us
+// (378 MB), 24576 x 2048 with channel scales in 30 us (150 MB), 8192 x 2048 in
+// 13.8 us (50 MB); 93, 46 and 15.3 us with the exact remainder for every value.
+// A few rows take 4.5 us, the latency of one pass.
 #include <algorithm>
 
 #include "common.h"

@@ -281,6 +281,18 @@ def test_linear_every_tile_height(cuda_ok, E, total, odd, N, K, dt):
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,total,odd,N,K", [
+    (24, 1800, (64, 65, 96, 97, 128, 129, 1, 33, 31), 8203, 200),        # a hundred rows, much work
+    (24, 5200, (1, 31, 33, 63, 65, 95, 97, 127, 129, 159, 161, 191, 193, 223, 225, 255, 257, 600),
+     14001, 129),                                                       # hundreds
+    (1, 0, (), 7300, 70),                                               # one matrix, 2300 rows
+])
+def test_linear_every_tile_height_with_many_channels(cuda_ok, E, total, odd, N, K, dt):
+    counts = [2300] if E == 1 else spread(E, total, E + K, list(odd))
+    check_linear(counts, N, K, dt, seed=E, div=3 if E > 1 else 1, src=E > 1)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("M,N,K", [(3, 100, 6000), (17, 40, 8192), (5, 33, 8300), (20, 130, 4100),
                                    (2100, 300, 5000), (1500, 2100, 70)])
 def test_linear_long_rows_and_many_rows(cuda_ok, M, N, K, dt):

@@ -496,7 +496,8 @@ moe_status moe_router_bwd(const moe_dims *dims, const void *x, const float *w_ro
  *   v times col_scale[e] per column       col_scale given, e the row's expert,
  *   scale[p] = max|v| / 127,  q[p][c] = v / scale[p] rounded to nearest (ties
  *   to even, as if from the exact quotient), in [-127, 127].
- * v and scale are float32.  A row of zeros has scale 0 and q 0; a row with a
+ * v and scale are float32, every operation of v rounded once (e^-z as expf gives
+ * it, within an ulp).  A row of zeros has scale 0 and q 0; a row with a
  * value that is not finite has scale NaN and q 0.
  *   act        moe_dtype of x and mul
  *   x, mul     act [M][K] with row strides ldx, ldm >= K (elements)

@@ -18,10 +18,13 @@
 // between the maximum and the quantization (their index is a compile-time
 // constant: an index that a loop runs past the array would move other
 // registers); what lies behind them, or is done again, is computed again.
-// Bound by memory where there are many rows: 98304 x 768 SwiGLU rows in 69 us
-// (378 MB), 24576 x 2048 with channel scales in 30 us (150 MB), 8192 x 2048 in
-// 13.8 us (50 MB); 93, 46 and 15.3 us with the exact remainder for every value.
-// A few rows take 4.5 us, the latency of one pass.
+// Bound by memory where there are many rows: 24576 x 2048 with channel scales in
+// 30 us (150 MB), 8192 x 2048 in 13.8 us (50 MB); 46 and 15.3 us with the exact
+// remainder for every value.  A few rows take 4.5 us, the latency of one pass.
+// SwiGLU rows are bound by the vector units: 98304 x 768 in 112 us (378 MB), of
+// which the exponential and the quotient in full float32 take 42 (69 us with the
+// hardware's exponential and reciprocal, whose error grows with |x| to 63
+// roundings at x = -80 and moved one value in 10^4 over a rounding border).
 #include <algorithm>
 
 #include "common.h"
@@ -115,12 +118,12 @@ __global__ __launch_bounds__(256, quant_waves(NT, NH, VEC, MODE)) void quant_i8_
   auto value = [&](const Chunk &C, int c, float *v) {
     C.x.get(c, A.K, v);
     if constexpr (SWIGLU) {
-      // (the hardware's exponential and reciprocal: a few roundings of v)
+      // (exactly this formula in float32: a value next to a border falls where
+      // the formula says, and gates far below 0 keep every bit)
       float m[8];
       C.u.get(c, A.K, m);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] *= __builtin_amdgcn_rcpf(1.0f + __expf(-v[i])) * m[i];
+      for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.0f + expf(-v[i])) * m[i];
     }
     if (scaled) {
       Values8<float, VEC> s;

@@ -175,6 +175,52 @@ def test_quant_swiglu(cuda_ok, M, K, dt):
     assert torch.all(q[:, K:] == 0)
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lo,hi", [(-30, -20), (-86, -70), (-86, 5)])
+@pytest.mark.parametrize("M,K", [(3, 300), (2100, 129), (2050, 768)])
+def test_quant_swiglu_negative_gates(cuda_ok, M, K, lo, hi, dt):
+    """Gates far below 0 in the whole row: the row's values are e^x in size, and
+    every one keeps float32's accuracy (expf 2 U, 1 + e, the quotient, the
+    product, the scale's quotient: 6 U)."""
+    g = gen(M + K)
+    gu = torch.rand(M, 2 * K, generator=g) * (hi - lo) + lo
+    gu[:, K:] = torch.randn(M, K, generator=g)
+    gu = gu.to(dt)
+    d = gu.to(DEV)
+    q, s = run_quant(d[:, :K], K, mul=d[:, K:])
+    x, u = gu[:, :K].double(), gu[:, K:].double()
+    v = x * torch.sigmoid(x) * u
+    amax = v.abs().max(1).values
+    assert torch.all((f64(s) - amax / 127).abs() <= 7 * U * amax / 127)
+    got = f64(q)[:, :K] * f64(s)[:, None]
+    assert torch.all((got - v).abs() <= f64(s)[:, None] * (0.5 + 127 * 8 * U) + 8 * U * v.abs())
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("K", [100, 129, 768, 4100])
+@pytest.mark.parametrize("M", [30, 2100])
+def test_quant_swiglu_with_channel_scales(cuda_ok, M, K, dt):
+    """SwiGLU and the expert's channel scales in one call; rows behind the last
+    expert stay as they were."""
+    E = 9
+    g = gen(M * K)
+    cut = torch.sort(torch.randint(0, M - 2, (E - 1,), generator=g)).values
+    off = torch.cat([torch.zeros(1), cut, torch.tensor([M - 3.0])]).to(torch.int32)
+    S = int(off[-1])
+    gu = (torch.randn(M, 2 * K, generator=g) * 3).to(dt)
+    cs = torch.rand(E, K, generator=g) + 0.1
+    d = gu.to(DEV)
+    q, s = run_quant(d[:, :K], K, mul=d[:, K:], col_scale=cs.to(DEV), offsets=off.to(DEV))
+    e = torch.searchsorted(off[1:].contiguous(), torch.arange(S, dtype=torch.int32), right=True)
+    x, u = gu[:S, :K].double(), gu[:S, K:].double()
+    v = x * torch.sigmoid(x) * u * cs[e].double()
+    amax = v.abs().max(1).values
+    assert torch.all((f64(s)[:S] - amax / 127).abs() <= 8 * U * amax / 127)   # (one product more)
+    got = f64(q)[:S, :K] * f64(s)[:S, None]
+    assert torch.all((got - v).abs() <= f64(s)[:S, None] * (0.5 + 127 * 9 * U) + 9 * U * v.abs())
+    assert torch.all(q[:S, K:] == 0) and torch.all(q[S:] == 55) and torch.all(s[S:] == -77)
+
+
 # ---------------------------------------------------------------- products --
 
 def linear_case(counts, N, K, dt, seed, div=1, pad=0, scales=True, src=True):

@@ -408,13 +408,17 @@ def _act_code(name, arg, t) -> int:
 
 def moe_quant_i8(x, q, scale, mul=None, col_scale=None, offsets=None, stream=None):
     """Rows of x (or silu(x) mul, or x col_scale[expert]) -> int8 rows q
-    [M][moe_i8_stride(K)] and their scales [M]."""
+    [M][moe_i8_stride(K)] or wider, one row after another (all of a row is
+    written: 0 behind column K), and their scales [M]."""
     f, dev, act = "moe_quant_i8", _gpu("moe_quant_i8", x), _act_code("moe_quant_i8", "x", x)
     M, K, ldx = _rows(f, "x", x, x.dtype, dev)
     Mq, Kq, ldq = _rows(f, "q", q, _I8, dev)
     if Mq != M or Kq < moe_i8_stride(K):
         raise MoeError(f"{f}: q must have {M} rows of at least {moe_i8_stride(K)} values, "
                        f"got {tuple(q.shape)}")
+    if ldq != Kq and M > 1:   # (the columns up to the stride would be another tensor's)
+        raise MoeError(f"{f}: q's rows must lie one after another, got {tuple(q.shape)} at "
+                       f"stride {ldq}")
     ldm, E = 0, 1
     if mul is not None:
         Mm, Km, ldm = _rows(f, "mul", mul, x.dtype, dev)
@@ -425,7 +429,7 @@ def moe_quant_i8(x, q, scale, mul=None, col_scale=None, offsets=None, stream=Non
     _call(f, dev, LIB.moe_quant_i8,
           (M, K, act, x.data_ptr(), ldx, _p(mul), ldm,
            _opt(f, "col_scale", col_scale, _F32, E * K, dev),
-           _opt(f, "offsets", offsets, _I32, E + 1, dev), E, q.data_ptr(), ldq,
+           _opt(f, "offsets", offsets, _I32, E + 1, dev), E, q.data_ptr(), Kq,
            _dense(f, "scale", scale, _F32, M, dev)), stream)
 
 

@@ -609,3 +609,21 @@ def test_binding_refuses_wrong_tensors(cuda_ok):
         B.moe_i8_linear(z(4, 128), z(4, dt=f), z(1, 40, 112), z(41, dt=f), z(4, 40, dt=f))
     with pytest.raises(B.MoeError, match="multiple of 16"):
         B.moe_i8_linear(z(4, 128), z(4, dt=f), z(1, 40, 100), None, z(4, 40, dt=f))
+
+
+def test_quant_writes_nothing_beside_its_rows(cuda_ok):
+    """q as a part of a wider buffer: rows that are not adjacent are refused,
+    one row is written to its own end."""
+    x = torch.randn(5, 100, generator=gen(3)).to(DEV)
+    room = torch.full((6, 384), 55, dtype=torch.int8, device=DEV)
+    for part in (room[:5, :128], room[:5, 128:256], room[1:6, 256:]):
+        with pytest.raises(B.MoeError, match="one after another"):
+            B.moe_quant_i8(x, part, torch.empty(5, device=DEV))
+    s = torch.empty(1, device=DEV)
+    B.moe_quant_i8(x[:1], room[5:, 128:256], s)
+    torch.cuda.synchronize()
+    rq, rs = quant_ref(x[:1].cpu())
+    assert torch.equal(room[5:, 128:228].cpu(), rq) and torch.equal(s.cpu(), rs)
+    assert torch.all(room[5, 228:256] == 0)
+    room[5, 128:256] = 55
+    assert torch.all(room == 55)

@@ -7,12 +7,20 @@ arithmetic of the layer happens here.
 """
 from __future__ import annotations
 
+import threading
+
 import numpy as np
 import torch
 
 from . import binding as B
 
 MATS = ("gate", "up", "down")
+MATS_I8 = ("gate_up", "down")   # of Int8Experts
+
+
+def _version(t) -> int:
+    """How often torch has written t (0 for a tensor that does not say)."""
+    return 0 if t.is_inference() else t._version
 
 
 def to_device(a, device):
@@ -240,7 +248,7 @@ class Int8Experts:
         self.gate_up, self.s_gate_up, self.down, self.s_down = gate_up, s_gate_up, down, s_down
         self.E, f2, self.d = gate_up.shape
         self.f = f2 // 2
-        self.t = None
+        self.t, self._from, self._lock = None, {}, threading.Lock()
 
     def _rows(self, M, K):
         dev = self.down.device
@@ -273,22 +281,52 @@ class Int8Experts:
         return gu
 
     def transpose(self):
-        """The matrices as the row gradients read them, laid out once (they
-        are frozen); rows padded to 16 bytes."""
-        def turned(w):
-            E, N, K = w.shape
-            room = torch.zeros(E, K, (N + 15) // 16 * 16, dtype=w.dtype, device=w.device)
-            room[:, :, :N] = w.transpose(1, 2)
-            return room[:, :, :N]
-        self.t = {"gate_up": turned(self.gate_up), "down": turned(self.down)}
+        """Lay out the matrices as the row gradients read them (rows padded to
+        16 bytes), once: they are frozen.  rows_grad does it by itself, again
+        for a matrix that has been replaced or that torch has written since;
+        after writes that torch does not count (a kernel's, inference mode's)
+        call this.  Waits for the GPU: what wrote the matrices and what still
+        reads an earlier layout is done before, and any stream may read the
+        layout afterwards.  Not inside a graph capture."""
+        with self._lock:
+            self._lay_out(MATS_I8)
+
+    def _lay_out(self, names):
+        dev = self.down.device
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("Int8Experts: call transpose() before the graph capture")
+        torch.cuda.synchronize(dev)
+        t = dict(self.t or {})
+        with torch.inference_mode(False):   # (a layout made in it could not be written again)
+            for name in names:
+                w, room = getattr(self, name), t.get(name)
+                E, N, K = w.shape
+                # (in place where it fits: a captured graph reads this memory)
+                if room is None or (room.shape, room.dtype, room.device) != \
+                        ((E, K, N), w.dtype, w.device):
+                    room = torch.zeros(E, K, (N + 15) // 16 * 16, dtype=w.dtype, device=w.device)
+                    room = room[:, :, :N]
+                room.copy_(w.transpose(1, 2))
+                t[name] = room
+                self._from[name] = (w, _version(w))
+        torch.cuda.synchronize(dev)
+        self.t = t
+
+    def _turned(self, name):
+        """The transposed matrix of `name` as it is now."""
+        w = getattr(self, name)
+        with self._lock:
+            kept = self._from.get(name)
+            if kept is None or kept[0] is not w or kept[1] != _version(w):
+                self._lay_out((name,))
+            return self.t[name]
 
     def rows_grad(self, which: str, dout, offsets, stream=None):
         """Gradient of the rows of the product `which` ("gate_up" or "down")
         for the gradient dout of its output, permuted order."""
-        if self.t is None:
-            self.transpose()
-        w, cs = self.t[which], self.s_gate_up if which == "gate_up" else self.s_down
+        cs = self.s_gate_up if which == "gate_up" else self.s_down
         with self._on(stream):
+            w = self._turned(which)
             q, s = self._rows(*dout.shape)
             dx = torch.empty(dout.shape[0], w.shape[1], dtype=dout.dtype, device=dout.device)
             B.moe_quant_i8(dout, q, s, col_scale=cs, offsets=offsets)

@@ -627,3 +627,89 @@ def test_quant_writes_nothing_beside_its_rows(cuda_ok):
     assert torch.all(room[5, 228:256] == 0)
     room[5, 128:256] = 55
     assert torch.all(room == 55)
+
+
+def large_experts(E=24, N=1024, K=2048, S=600, seed=7):
+    """Down products whose layout takes the GPU a while, and a gradient of them."""
+    from sparse_moe_expert_fp32_amd.layer import Int8Experts
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    w = torch.randint(-127, 128, (E, N, K), generator=g, dtype=torch.int8, device=DEV)
+    gu = torch.randint(-127, 128, (E, 2 * K, 128), generator=g, dtype=torch.int8, device=DEV)
+    cs = (torch.rand(E, N, generator=g, device=DEV) + 0.5) / 1000
+    off = torch.linspace(0, S, E + 1, device=DEV).to(torch.int32)
+    dout = torch.randn(S, N, generator=g, device=DEV).bfloat16()
+    return Int8Experts(gu, torch.ones(E, 2 * K, device=DEV), w, cs), dout, off
+
+
+def rows_grad_ref(X, dout, off):
+    """The quantized definition in float64, on the CPU's quantizer."""
+    out, at = torch.zeros(dout.shape[0], X.down.shape[2], dtype=torch.float64), off.tolist()
+    for e in range(X.E):
+        i, j = at[e], at[e + 1]
+        q, s = quant_ref(dout[i:j].float().cpu() * X.s_down[e].cpu())
+        out[i:j] = (q.double() @ X.down[e].cpu().double()) * s.double()[:, None]
+    return out
+
+
+def near_bf16(got, ref):
+    return bool(torch.all((f64(got) - ref).abs() <= ref.abs() * (HALF[torch.bfloat16] + 4 * U)))
+
+
+def test_row_gradient_first_on_a_side_stream(cuda_ok):
+    """The first call, which lays the matrices out, on a side stream while the
+    current one is busy; then calls on other streams, which find the layout."""
+    X, dout, off = large_experts()
+    ref = rows_grad_ref(X, dout, off)
+    torch.cuda.synchronize()
+    s, s2, busy = torch.cuda.Stream(), torch.cuda.Stream(), torch.randn(4096, 4096, device=DEV)
+    for _ in range(20):
+        busy = busy @ busy * 1e-3
+    s.wait_stream(torch.cuda.current_stream())
+    first = X.rows_grad("down", dout, off, stream=s)
+    other = X.rows_grad("down", dout, off, stream=s2)
+    here = X.rows_grad("down", dout, off)
+    torch.cuda.synchronize()
+    assert near_bf16(first, ref)
+    assert torch.equal(first, here) and torch.equal(first, other)
+
+
+def test_row_gradient_follows_its_matrices(cuda_ok):
+    """Matrices written in place or replaced after a first gradient."""
+    X, dout, off = large_experts(E=5, N=272, K=160, S=90)
+    assert near_bf16(X.rows_grad("down", dout, off), rows_grad_ref(X, dout, off))
+    X.down.copy_(torch.flip(X.down, (2,)))
+    assert near_bf16(X.rows_grad("down", dout, off), rows_grad_ref(X, dout, off))
+    X.down = torch.flip(X.down, (1,)).contiguous()
+    assert near_bf16(X.rows_grad("down", dout, off), rows_grad_ref(X, dout, off))
+    with torch.inference_mode():
+        X.down = torch.flip(X.down, (1,)).contiguous()
+        assert near_bf16(X.rows_grad("down", dout, off), rows_grad_ref(X, dout, off))
+        X.down.zero_()
+    X.transpose()
+    assert not X.rows_grad("down", dout, off).any()
+
+
+def test_row_gradient_in_a_graph(cuda_ok):
+    """A capture needs the layout before it; the captured product reads the
+    layout that transpose() renews in place."""
+    X, dout, off = large_experts(E=5, N=256, K=128, S=90)
+    dx, y = torch.zeros(90, 128, dtype=torch.bfloat16, device=DEV), torch.zeros(4, device=DEV)
+    B.moe_quant_i8(dout, torch.empty(90, 256, dtype=torch.int8, device=DEV),
+                   torch.empty(90, device=DEV))   # (the library is loaded on this GPU)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        y.add_(1)
+        with pytest.raises(RuntimeError, match="transpose"):
+            X.rows_grad("down", dout, off)
+    X.transpose()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dx.copy_(X.rows_grad("down", dout, off))
+    for step in range(4):
+        ref = X.rows_grad("down", dout, off)
+        dx.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dx, ref) and near_bf16(dx, rows_grad_ref(X, dout, off))
+        X.down.copy_(torch.flip(X.down, (1 + step % 2,)))
+        X.transpose()

@@ -151,13 +151,14 @@ class DeviceLayer:
     # ---- router training: load-balance loss and the router's own gradients
     def init_router_training(self):
         """Buffers of the load-balance loss and the router's gradients (the
-        layer needs want_logits=True and a backward)."""
+        layer needs want_logits=True and a backward).  bal_dloss, the weight of
+        the balance loss in the whole loss, is 0 until the caller fills it."""
         if self.logits is None or self.save is None:
             raise ValueError("router training needs want_logits=True and a layer with a backward")
         cfg, new = self.cfg, lambda *n, dt=torch.float32: torch.empty(n, dtype=dt, device=self.dev)
         self.bal_loss, self.bal_counts = new(1), new(cfg.E + 1, dt=torch.int32)
         self.bal_prob, self.bal_stats = new(cfg.E), new(cfg.T, 2)
-        self.bal_dloss = new(1)
+        self.bal_dloss = torch.zeros(1, device=self.dev)
         self.dlogits_bal, self.dlogits = new(cfg.T, cfg.E), new(cfg.T, cfg.E)
         self.dw_router = new(cfg.d, cfg.E)
         self.db_router = new(cfg.E) if self.t.get("b_router") is not None else None

@@ -403,6 +403,24 @@ def test_router_training_dx_adds_the_balance_share(cuda_ok):
     assert torch.all((f64(L.dx) - ref).abs() <= 2.0 ** -8 * ref.abs() * 1.01 + 1e-6 * share.abs().max())
 
 
+def test_router_training_without_a_balance_weight(cuda_ok):
+    """A step whose caller has filled no bal_dloss: the balance loss weighs
+    nothing, whatever the memory held."""
+    cfg, L = layer()
+    torch.use_deterministic_algorithms(True)      # (fills new memory with NaN)
+    try:
+        L.init_router_training()
+    finally:
+        torch.use_deterministic_algorithms(False)
+    L.train_step()
+    torch.cuda.synchronize()
+    dx = L.dx.clone()
+    L.router_train_step()
+    torch.cuda.synchronize()
+    assert float(L.bal_dloss) == 0 and torch.all(L.dlogits_bal == 0)
+    assert torch.equal(L.dx, dx) and torch.isfinite(L.dw_router).all()
+
+
 def test_router_training_on_a_side_stream_and_in_a_graph(cuda_ok):
     """The step captured once and replayed between eager steps of the same
     layer gives the eager bits on every replay."""

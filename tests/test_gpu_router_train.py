@@ -14,6 +14,7 @@ pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
 DEV = "cuda:0"
+HALF_ACT = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
 
 
 def gen(seed):
@@ -342,6 +343,48 @@ def test_router_bwd_variants(cuda_ok, act, kw):
     elif kw.get("valid"):
         kw["valid"] = torch.rand(150, generator=gen(4)) > 0.3
     check_router(150, 224, 70, act, **kw)
+
+
+def same_or_near(got, ref, tol):
+    """Infinities and NaN as in ref, the rest within tol."""
+    got = f64(got)
+    assert torch.equal(got.isnan(), ref.isnan())
+    assert torch.equal(got.isinf(), ref.isinf()) and torch.equal(got[ref.isinf()], ref[ref.isinf()])
+    fin = ref.isfinite()
+    assert torch.all(((got - ref).abs() <= tol)[fin])
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d,E", [(12, 64, 1), (70, 96, 20), (300, 256, 130), (600, 160, 65)])
+def test_router_bwd_infinities(cuda_ok, T, d, E, act, masked):
+    """Infinities and NaN in rows that take part give what float32 sums give
+    and stay in their rows and columns; in masked rows they reach nothing."""
+    x, w, dl, dx_in = router_case(T, d, E, act, T * d)
+    x[3, 5], x[4, 7], x[9, 30] = np.inf, -np.inf, np.nan
+    x[1, 2] = np.inf
+    dl[1] = torch.where(torch.arange(E) % 2 == 0, 0.5, -2.0)     # (one bf16 plane)
+    x[8, 40] = np.inf
+    dl[8] = 0
+    dl[2, 0], dl[6, E - 1] = -np.inf, np.nan
+    w[1, 0], w[8, E - 1] = np.inf, np.nan
+    dx_in[5, 3] = -np.inf
+    valid = torch.arange(T) % 4 != 2 if masked else None
+    if masked:      # (the rows 2 and 6 of dl are masked now; so is this one)
+        x[10], dl[10] = np.nan, np.inf
+    dx, dw, db = run_router(dims(T, d, E, 1, act), x, w, valid, dl, dx_in, "xwb")
+    on = torch.ones(T, dtype=torch.bool) if valid is None else valid
+    xd, dld, wd = x[on].double(), dl[on].double(), w.double()
+    share = dld[:, None, :] * wd[None]
+    ref, mag = dx_in.double(), torch.zeros(T, d, dtype=torch.float64)
+    ref[on] += share.sum(2)
+    mag[on] = share.abs().sum(2)
+    half = HALF_ACT[act]
+    same_or_near(dx, ref, half * ref.abs() * (1 + half) + (E + 8) * U * (mag + ref.abs()) +
+                 (2.0 ** -15 * mag if act == "bf16" else 0))
+    prod = xd[:, :, None] * dld[:, None, :]
+    same_or_near(dw, prod.sum(0), (T + 12) * U * prod.abs().sum(0))
+    same_or_near(db, dld.sum(0), (T + 12) * U * dld.abs().sum(0))
 
 
 def test_router_bwd_is_repeatable(cuda_ok):

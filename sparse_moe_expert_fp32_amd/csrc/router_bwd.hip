@@ -168,14 +168,18 @@ void launch_gate_bwd(bool bf16, const void *dy, const void *e_out, const int32_t
 
 // ---- the two products in float32 accuracy on the bf16 matrix cores.
 //
-// A float32 value is the sum of three bf16 values exactly (8 + 8 + 8 bits of
-// its significand, cut off, not rounded), a bf16 value is one.  So
+// A float32 value is the sum of three bf16 values exactly: each plane is what is
+// left, rounded to nearest (at most 2^-8 of the value is left behind the first
+// plane, 2^-17 behind the second, with either sign), a bf16 value is one.  So
 //   C[m][n] = sum_k A(m, k) B(n, k)
-// is the sum of the products of such planes; the planes i, j with i + j < 3
-// are kept for float32 results (what is left out is below 2^-24 of a product),
-// and i + j < 2 for results that are rounded to bf16 (two planes, the second
-// one rounded: 2^-16).  Three matrix instructions of 16 clocks in the place of
-// the eight of 32 that float32 operands take (v_mfma_f32_16x16x4_f32).
+// is the sum of the products of such planes.  The planes i, j with i + j < 3 are
+// kept for float32 results: what is left out is at most 2^-24 (1 + 2^-10) of a
+// product, of either sign.  i + j < 2 with two planes are kept for results that
+// are rounded to bf16: 2^-17 for the rounding of each operand's second plane and
+// 2^-16 left out, 2^-15 of a product in all.  (Planes cut off instead of rounded
+// left out up to 2^-21 and 2^-14, always towards 0.)  Three matrix instructions
+// of 16 clocks in the place of the eight of 32 that float32 operands take
+// (v_mfma_f32_16x16x4_f32).
 //
 // 128 x BN tile per block of four waves (2 x 2), two blocks per CU, steps of 32
 // along k through two LDS slots; two steps are on their way while one is
@@ -193,7 +197,8 @@ DEV uint8_t *rb_place(uint8_t *lds, int r, int c) {
   return lds + r * 64 + ((c ^ rb_swz(r)) & 3) * 16;
 }
 
-// W values -> planes of W bf16 (W / 2 words each)
+// W values -> planes of W bf16 (W / 2 words each).  A value that rounds to
+// infinity leaves planes whose sums are not finite; those are taken again.
 template <int P, int W> DEV void split(const float *f, uint32_t (&o)[P][W / 2]) {
   float r[W];
 #pragma unroll
@@ -202,15 +207,10 @@ template <int P, int W> DEV void split(const float *f, uint32_t (&o)[P][W / 2]) 
   for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int i = 0; i < W / 2; ++i) {
-      const uint32_t lo = __float_as_uint(r[2 * i]), hi = __float_as_uint(r[2 * i + 1]);
-      if (p == 1 && P == 2) {
-        o[p][i] = cvt_pk_bf16(r[2 * i], r[2 * i + 1]);
-      } else {
-        o[p][i] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);   // the upper halves
-        if (p + 1 < P) {
-          r[2 * i] -= __uint_as_float(lo & 0xFFFF0000u);
-          r[2 * i + 1] -= __uint_as_float(hi & 0xFFFF0000u);
-        }
+      o[p][i] = cvt_pk_bf16(r[2 * i], r[2 * i + 1]);
+      if (p + 1 < P) {
+        r[2 * i] -= __uint_as_float(o[p][i] << 16);
+        r[2 * i + 1] -= __uint_as_float(o[p][i] & 0xFFFF0000u);
       }
     }
 }
@@ -451,8 +451,9 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(RouterGemmArgs G) {
     return m0 + (OA::PAIR ? 2 * rl + wm : 64 * wm + rl);
   };
   auto col_of = [&](int n) { return n0 + (BN / 2) * wn + 16 * n + 4 * lg; };
-  // Planes do not carry what is not finite: an infinity leaves NaN in its lower
-  // planes and meets zeros in the other operand's.  Sums that are not finite are
+  // Planes do not carry what is not finite: an infinity (or a value that rounds to
+  // one) leaves NaN in its lower planes and meets zeros in the other operand's, and
+  // a first plane's product may pass the largest number.  Sums that are not finite are
   // taken again from the values, in float32, by the waves that have any (a row
   // that does not take part has no terms).  Nothing where all is finite; with a
   // whole row of x NaN, 8192 x 2048 x 460 takes 3.9 ms in the place of 0.25.

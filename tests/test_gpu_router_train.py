@@ -387,6 +387,76 @@ def test_router_bwd_infinities(cuda_ok, T, d, E, act, masked):
     same_or_near(db, dld.sum(0), (T + 12) * U * dld.abs().sum(0))
 
 
+def hard_values(n, seed):
+    """Significands whose lower bits are most when the leading 8 or 16 are
+    taken off: just below and above the steps of bf16, all ones, random ones."""
+    g = gen(seed)
+    near = torch.tensor([2.0 ** -7 - 2.0 ** -23, 2.0 ** -8 - 2.0 ** -23, 2.0 ** -8 + 2.0 ** -23,
+                         2.0 ** -7 + 2.0 ** -15 - 2.0 ** -23, 2.0 ** -8 + 2.0 ** -16 + 2.0 ** -23,
+                         1 - 2.0 ** -23, 2.0 ** -7 - 2.0 ** -16 - 2.0 ** -22, 2.0 ** -6 - 2.0 ** -23])
+    v = 1 + torch.where(torch.rand(n, generator=g) < 0.5, near[torch.randint(0, 8, (n,), generator=g)],
+                        torch.rand(n, generator=g) * 2.0 ** -6)
+    return v * 2.0 ** torch.randint(-20, 20, (n,), generator=g) * torch.sign(torch.randn(n, generator=g))
+
+
+def test_router_bwd_single_products_keep_float32(cuda_ok):
+    """One product per sum: at most 2^-24 of it left out (1 U, and 2^-10 of
+    that), five additions of plane products to the sum (5 U)."""
+    T, d, E = 300, 256, 130
+    dl, w = hard_values(T, 1)[:, None], hard_values(d, 2)[:, None]
+    dx, _, _ = run_router(dims(T, d, 1, 1, "f32"), torch.zeros(T, d), w, None, dl, None, "x")
+    ref = dl.double() @ w.double().t()
+    assert torch.all((f64(dx) - ref).abs() <= 7 * U * ref.abs())
+    for n, act in ((E, "f32"), (7, "f32"), (E, "bf16")):
+        x, dl = hard_values(d, 3)[None].to(act_t(act)), hard_values(n, 4)[None]
+        _, dw, _ = run_router(dims(1, d, n, 1, act), x, torch.zeros(d, n), None, dl, None, "w")
+        ref = x.double().t() @ dl.double()
+        assert torch.all((f64(dw) - ref).abs() <= 7 * U * ref.abs())
+
+
+def test_router_bwd_bf16_dx_where_the_sum_cancels(cuda_ok):
+    """dx_in takes the product's bf16 value off, so that the operands' 16 bits
+    show: 2^-17 of each (rounded), 2^-16 for the product of what is below their
+    leading 8 bits, float32 additions, one rounding of what is left."""
+    T, d = 300, 256
+    dl, w = hard_values(T, 5)[:, None], hard_values(d, 6)[:, None]
+    prod = dl.double() @ w.double().t()
+    dx_in = (-prod).to(torch.bfloat16)
+    dx, _, _ = run_router(dims(T, d, 1, 1, "bf16"), torch.zeros(T, d).bfloat16(), w, None, dl, dx_in, "x")
+    ref = prod + dx_in.double()
+    tol = (2.0 ** -15 * (1 + 2.0 ** -7) + 8 * U) * prod.abs()
+    assert torch.all((f64(dx) - ref).abs() <= tol + 2.0 ** -8 * (ref.abs() + tol))
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_router_bwd_next_to_the_largest_number(cuda_ok, act):
+    """Operands and sums that a rounding to 8 bits would take to infinity."""
+    T, d, E = 40, 64, 33
+    big = torch.finfo(torch.float32).max
+    x, w, dl = torch.zeros(T, d), torch.zeros(d, E), torch.zeros(T, E)
+    dl[3, 4], dl[5, 6], dl[7, 8] = big, -big * (1 - 2.0 ** -9), 2.0 ** -100
+    w[1, 4], w[2, 6], w[3, 4] = 2.0 ** -110, 1.0, 0.75
+    w[5, 4] = 2.0                         # (past the largest number: infinite)
+    x[3, 9], x[5, 10], x[7, 11] = 2.0 ** -100, 1.0, 2.0 ** 127
+    if act == "f32":
+        w[4, 8], x[7, 12] = big, big
+    x = x.to(act_t(act))
+    dx, dw, _ = run_router(dims(T, d, E, 1, act), x, w, None, dl, None, "xw")
+    rx, rw = dl.double() @ w.double().t(), x.double().t() @ dl.double()
+    rx[rx > big] = np.inf
+    half = HALF_ACT[act]
+    if act == "bf16":
+        # bf16's last step ends at top; operands kept to 16 bits move a sum by up
+        # to 2^-15 of it, so one that is 2^-24 from top may end on either side
+        top = (2 - 2.0 ** -8) * 2.0 ** 127
+        edge = (rx.abs() / top - 1).abs() <= 2.0 ** -15
+        assert int(edge.sum()) == 1 and float(f64(dx)[edge].abs()) >= top * (1 - 2.0 ** -8)
+        dx = torch.where(edge.to(DEV), 0, dx)
+        rx = torch.where(edge, 0.0, torch.where(rx.abs() >= top, torch.sign(rx) * np.inf, rx))
+    same_or_near(dx, rx, (half + 7 * U + (2.0 ** -15 * 1.01 if act == "bf16" else 0)) * rx.abs())
+    same_or_near(dw, rw, 7 * U * rw.abs())
+
+
 def test_router_bwd_is_repeatable(cuda_ok):
     x, w, dl, dx_in = router_case(2000, 256, 100, "bf16", 9)
     a = run_router(dims(2000, 256, 100, 1), x, w, None, dl, dx_in, "xwb")

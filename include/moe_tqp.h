@@ -474,7 +474,8 @@ moe_status moe_gate_bwd(const moe_dims *dims, const void *dy, const void *e_out,
  * db_router have the router's layouts, ready for moe_adamw_step.  The weight
  * and bias gradients, and dx in MOE_F32, keep float32 accuracy; for a dx in
  * bf16 the products of D W_r^T are taken to 15 bits (2^-15 of each), summed in
- * float32 and the result is rounded once.  Infinities and NaN of tokens that take part give
+ * float32 and the result is rounded once.  What an operand holds below 2^-133
+ * (bf16's least step) is lost.  Infinities and NaN of tokens that take part give
  * what a float32 sum gives.
  *   x          act [T][d], 16-byte aligned; read only for dw_router
  *   w_router   f32 [d][E]; read only for dx

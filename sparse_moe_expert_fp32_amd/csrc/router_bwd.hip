@@ -62,7 +62,7 @@ template <typename T, int KM>
 __global__ __launch_bounds__(256) void gate_bwd_kernel(
     const T *__restrict__ dy, const T *__restrict__ e_out, const int32_t *__restrict__ topk_idx,
     const float *__restrict__ gates, const int32_t *__restrict__ slot_pos,
-    const uint8_t *__restrict__ valid, const float *dl_in, int Tn, int d, int E, int k,
+    const uint8_t *__restrict__ valid, const float *dl_in, int Tn, int S, int d, int E, int k,
     float *dl_out) {
   constexpr int V = V16<T>::N, NE = 8;
   const int lane = threadIdx.x & 63;
@@ -74,7 +74,7 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(
     return;
   }
   // lane j < k: slot j of the token (indices kept in range)
-  const int S = Tn * k, at = min(lane, k - 1);
+  const int at = min(lane, k - 1);
   const int ej = min(max(topk_idx[(size_t)t * k + at], 0), E - 1);
   const int pj = min(max(slot_pos[(size_t)t * k + at], 0), S - 1);
   const float gj = lane < k ? gates[(size_t)t * k + at] : 0.f;
@@ -152,18 +152,25 @@ void launch_gate_bwd(bool bf16, const void *dy, const void *e_out, const int32_t
                      const float *gates, const int32_t *slot_pos, const uint8_t *valid,
                      const float *dl_in, int T, int d, int E, int k, float *dl_out,
                      hipStream_t st) {
-  const int grid = (T + 3) / 4;
+  constexpr int kTokens = 1 << 24;   // per launch: a grid's threads are counted in 32 bits
+  const int S = T * k;
+  for (int t0 = 0; t0 < T; t0 += kTokens) {
+    const int n = std::min(kTokens, T - t0), grid = (n + 3) / 4;
+    const size_t slot = (size_t)t0 * k, row = (size_t)t0 * E;
 #define MOE_GB(TY, KM) gate_bwd_kernel<TY, KM><<<grid, 256, 0, st>>>( \
-      (const TY *)dy, (const TY *)e_out, topk_idx, gates, slot_pos, valid, dl_in, T, d, E, k, dl_out)
+      (const TY *)dy + (size_t)t0 * d, (const TY *)e_out, topk_idx + slot, gates + slot, \
+      slot_pos + slot, valid ? valid + t0 : nullptr, dl_in ? dl_in + row : nullptr, n, S, d, E, k, \
+      dl_out + row)
 #define MOE_GBK(TY)          \
   if (k <= 2) MOE_GB(TY, 2); \
   else if (k <= 4) MOE_GB(TY, 4); \
   else if (k <= 6) MOE_GB(TY, 6); \
   else if (k <= 8) MOE_GB(TY, 8); \
   else MOE_GB(TY, 12);
-  if (bf16) { MOE_GBK(bf16_t) } else { MOE_GBK(float) }
+    if (bf16) { MOE_GBK(bf16_t) } else { MOE_GBK(float) }
 #undef MOE_GBK
 #undef MOE_GB
+  }
 }
 
 // ---- the two products in float32 accuracy on the bf16 matrix cores.

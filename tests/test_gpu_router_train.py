@@ -271,6 +271,28 @@ def test_gate_bwd_variants(cuda_ok, kw):
     check_gate(50, 160, 70, 6, "bf16", **kw)
 
 
+def test_gate_bwd_most_tokens(cuda_ok):
+    """2^26 slots, one a token: more than a launch takes."""
+    T, d = 1 << 26, 32
+    g = torch.Generator(device=DEV).manual_seed(1)
+    new = lambda *n: torch.randn(*n, generator=g, device=DEV, dtype=torch.bfloat16)  # noqa: E731
+    dy, e_out = new(T, d), new(T, d)
+    gates = torch.rand(T, generator=g, device=DEV)
+    idx = torch.zeros(T, dtype=torch.int32, device=DEV)
+    pos = torch.arange(T - 1, -1, -1, dtype=torch.int32, device=DEV)
+    valid = torch.ones(T, dtype=torch.uint8, device=DEV)
+    valid[5], valid[T - 7] = 0, 0
+    out = torch.full((T, 1), -77.0, device=DEV)
+    B.moe_gate_bwd(dims(T, d, 1, 1), dy, e_out, idx, gates, pos, valid, None, out)
+    for t in (0, (1 << 24) - 500, 1 << 25, T - 1000):      # (both sides of a launch's end)
+        s = slice(t, t + 1000)
+        prod = dy[s].double() * e_out[pos[s].long()].double()
+        dg, mag, ga = prod.sum(1), prod.abs().sum(1), gates[s].double()
+        ref = torch.where(valid[s] > 0, ga * (dg - ga * dg), 0.0)
+        assert torch.all((out[s, 0].double() - ref).abs() <= 32 * U * ga * mag * 2)
+    assert int((out == -77).sum()) == 0
+
+
 # ------------------------------------------------------------------- router --
 
 def router_case(T, d, E, act, seed):

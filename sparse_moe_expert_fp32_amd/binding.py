@@ -442,8 +442,7 @@ def moe_i8_linear(a, a_scale, w, w_scale, out, offsets=None, row_src=None, row_d
     M, N, ldo = _rows(f, "out", out, out.dtype, dev)
     E, Nw, K = w.shape if w.dim() == 3 else (0, 0, 0)
     es, ldw, one = w.stride() if E else (0, 0, 0)
-    if not E or Nw != N or (w.dtype is not _I8 and w.dtype is not _U8) or \
-            w.get_device() != dev or (one != 1 and K > 1):
+    if not E or Nw != N or w.dtype is not _I8 or w.get_device() != dev or (one != 1 and K > 1):
         raise MoeError(f"{f}: w must be int8 [E][{N}][K] with adjacent columns on GPU {dev}, got "
                        f"{w.dtype} {tuple(w.shape)} {w.stride()} on {w.device}")
     if K % 16 or not w.is_contiguous():

@@ -713,3 +713,15 @@ def test_row_gradient_in_a_graph(cuda_ok):
         assert torch.equal(dx, ref) and near_bf16(dx, rows_grad_ref(X, dout, off))
         X.down.copy_(torch.flip(X.down, (1 + step % 2,)))
         X.transpose()
+
+
+def test_linear_refuses_unsigned_matrices(cuda_ok):
+    """uint8 values have no sign to read; their bytes do, as a view in int8."""
+    w = torch.arange(256, device=DEV).repeat(1, 4, 1).to(torch.uint8)
+    a = torch.ones(2, 256, dtype=torch.int8, device=DEV)
+    out = torch.zeros(2, 4, device=DEV)
+    with pytest.raises(B.MoeError, match="w must be int8"):
+        B.moe_i8_linear(a, torch.ones(2, device=DEV), w, None, out)
+    assert not out.any()
+    B.moe_i8_linear(a, torch.ones(2, device=DEV), w.view(torch.int8), None, out)
+    assert torch.all(out == -128)

@@ -485,7 +485,8 @@ moe_status moe_gate_bwd(const moe_dims *dims, const void *dy, const void *e_out,
  *   dx_in      act [T][d] or NULL (0), 16-byte aligned
  *   dx         act [T][d] (out) or NULL, 16-byte aligned; may be dx_in
  *   dw_router  f32 [d][E] (out) or NULL;  db_router f32 [E] (out) or NULL
- *   ws         moe_workspace_size(MOE_CALL_ROUTER_BWD) bytes, 16-byte aligned */
+ *   ws         moe_workspace_size(MOE_CALL_ROUTER_BWD) bytes, 16-byte aligned;
+ *              only for dw_router (any value without it) */
 moe_status moe_router_bwd(const moe_dims *dims, const void *x, const float *w_router,
                           const uint8_t *valid, const float *dlogits, const void *dx_in, void *dx,
                           float *dw_router, float *db_router, void *ws, size_t ws_bytes,

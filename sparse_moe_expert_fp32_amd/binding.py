@@ -436,7 +436,9 @@ def moe_quant_i8(x, q, scale, mul=None, col_scale=None, offsets=None, stream=Non
 def moe_i8_linear(a, a_scale, w, w_scale, out, offsets=None, row_src=None, row_div=1,
                   stream=None):
     """out[p] = rows a (int8, as moe_quant_i8 writes them) by the int8 matrix
-    w[e] [N][K] of the row's expert, scaled per row and per channel."""
+    w[e] [N][K] of the row's expert, scaled per row and per channel.  (Rows and
+    scales of a float matrix come from moe_quant_i8 over its output channels;
+    two's-complement bytes kept as uint8 go in as w.view(torch.int8).)"""
     f, dev, act = "moe_i8_linear", _gpu("moe_i8_linear", a), _act_code("moe_i8_linear", "out", out)
     R, Ka, lda = _rows(f, "a", a, _I8, dev)
     M, N, ldo = _rows(f, "out", out, out.dtype, dev)

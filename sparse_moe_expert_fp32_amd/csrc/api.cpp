@@ -1111,8 +1111,10 @@ moe_status moe_router_bwd(const moe_dims *dims, const void *x, const float *w_ro
   REQUIRE(!dw_router || x, "moe_router_bwd: x required when dw_router is requested");
   REQUIRE((((uintptr_t)x | (uintptr_t)dx_in | (uintptr_t)dx) & 15) == 0,
           "moe_router_bwd: x, dx_in and dx must be 16-byte aligned");
-  TRY(check_ws(dims, MOE_CALL_ROUTER_BWD, ws, ws_bytes));
-  REQUIRE(((uintptr_t)ws & 15) == 0, "moe_router_bwd: ws must be 16-byte aligned");
+  if (dw_router) {   // (only its partial sums stand in the workspace)
+    TRY(check_ws(dims, MOE_CALL_ROUTER_BWD, ws, ws_bytes));
+    REQUIRE(((uintptr_t)ws & 15) == 0, "moe_router_bwd: ws must be 16-byte aligned");
+  }
   moe::launch_router_bwd(dims->act == MOE_BF16, x, w_router, valid, dlogits, dx_in, dims->T,
                          dims->d_model, dims->n_experts, dx, dw_router, db_router, ws,
                          (hipStream_t)stream);

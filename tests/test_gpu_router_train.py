@@ -479,6 +479,22 @@ def test_router_bwd_next_to_the_largest_number(cuda_ok, act):
     same_or_near(dw, rw, 7 * U * rw.abs())
 
 
+def test_router_bwd_workspace_is_for_the_weight_gradient(cuda_ok):
+    """dx and db alone need none; dw_router without one is refused."""
+    T, d, E = 2000, 96, 20
+    x, w, dl, dx_in = router_case(T, d, E, "bf16", 3)
+    dm = dims(T, d, E, 1)
+    assert B.moe_workspace_size(dm, B.CALL_ROUTER_BWD) > 0
+    ref_dx, _, ref_db = run_router(dm, x, w, None, dl, dx_in, "xb")
+    t = [v.to(DEV) for v in (x, w, dl, dx_in)]
+    dx, dw, db = torch.empty_like(t[0]), torch.empty_like(t[1]), torch.empty(E, device=DEV)
+    B.moe_router_bwd(dm, None, t[1], None, t[2], t[3], dx, None, db, None)
+    torch.cuda.synchronize()
+    assert torch.equal(dx, ref_dx) and torch.equal(db, ref_db)
+    with pytest.raises(B.MoeError, match="workspace"):
+        B.moe_router_bwd(dm, t[0], t[1], None, t[2], t[3], dx, dw, db, None)
+
+
 def test_router_bwd_is_repeatable(cuda_ok):
     x, w, dl, dx_in = router_case(2000, 256, 100, "bf16", 9)
     a = run_router(dims(2000, 256, 100, 1), x, w, None, dl, dx_in, "xwb")

@@ -296,7 +296,7 @@ DEV int tl_swz_w(int r) { return ((r >> 2) & 6) | ((r >> 1) & 1); }
 
 constexpr int kWaitLds = 0xC07F;   // s_waitcnt lgkmcnt(0), nothing else
 
-template <typename T, int MI>
+template <typename T, int MI, typename Off>
 DEV void row_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds) {
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
   const int w = tid >> 6, wm = w & 1, wn = w >> 1;
@@ -308,21 +308,21 @@ DEV void row_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
   const int a_get = TL_A + ar * TL_KS + (lg ^ tl_swz_a(ar)) * 16;
   const int w_get = wr * TL_KS + (lg ^ tl_swz_w(wr)) * 16;
   // byte offsets inside the matrix, and inside a (from the tile's first row
-  // on, where the rows are not looked up), are below 2^32 (launch_linear)
+  // on, where the rows are not looked up): 32 bits, or 64 (launch_linear)
   const int first = A.row_src ? 0 : R.p0;
   const int8_t *ab = A.a + (size_t)first * A.lda;
   const int8_t *we = A.w + (size_t)R.e * A.N * A.ldw;
-  uint32_t ao[MI], wo[4];
+  Off ao[MI], wo[4];
   int rows[MI + 1], from[MI + 1];   // this thread's pieces, and the row whose scale it fetches
 #pragma unroll
   for (int i = 0; i < MI; ++i) rows[i] = min(R.p0 + tr + 32 * i, R.end - 1);
   rows[MI] = min(R.p0 + tid, R.end - 1);
   source_rows(A, rows, from);
 #pragma unroll
-  for (int i = 0; i < MI; ++i) ao[i] = (uint32_t)(from[i] - first) * (uint32_t)A.lda + 16 * tc;
+  for (int i = 0; i < MI; ++i) ao[i] = (Off)(from[i] - first) * (Off)A.lda + 16 * tc;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    wo[i] = (uint32_t)min(n0 + tr + 32 * i, A.N - 1) * (uint32_t)A.ldw;
+    wo[i] = (Off)min(n0 + tr + 32 * i, A.N - 1) * (Off)A.ldw;
   // The rows of the next step and the channels of the next two are on their
   // way (the matrix comes from HBM, whose latency is longer than a step).
   uint4 sa_[MI], w0[4], w1[4];
@@ -450,8 +450,9 @@ DEV void row_tile(const LinearI8Args &A, const RowTile &R, int n0, uint8_t *lds)
 // one's channels on their way during the end of the last: what the shorter
 // start saves, 418 -> 368 us for 98304 rows by 460 matrices of 2048 x 768, the
 // registers held over that end cost again; one tile a block takes 365.)
-template <typename T, int NC, int BM>
-__global__ __launch_bounds__(256, BM <= 64 ? 4 : BM == 128 ? 3 : 2) void linear_i8_tiled_kernel(LinearI8Args A) {
+template <typename T, int NC, int BM, typename Off>
+__global__ __launch_bounds__(256, BM <= 64 ? 4 : BM == 128 && sizeof(Off) == 4 ? 3 : 2)
+void linear_i8_tiled_kernel(LinearI8Args A) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[tl_lds(BM)];
   const int nt = (A.N + TL_BN - 1) / TL_BN;
   RowTile R;
@@ -467,26 +468,27 @@ __global__ __launch_bounds__(256, BM <= 64 ? 4 : BM == 128 ? 3 : 2) void linear_
   }
   const int rows = R.end - R.p0;
   if constexpr (BM <= 64) {
-    row_tile<T, BM / 32>(A, R, n0, lds);
+    row_tile<T, BM / 32, Off>(A, R, n0, lds);
   } else {
-    if (rows <= 32) row_tile<T, 1>(A, R, n0, lds);
-    else if (rows <= 64) row_tile<T, 2>(A, R, n0, lds);
-    else if (rows <= 96) row_tile<T, 3>(A, R, n0, lds);
-    else if constexpr (BM == 128) row_tile<T, 4>(A, R, n0, lds);
-    else if (rows <= 128) row_tile<T, 4>(A, R, n0, lds);
-    else if (rows <= 160) row_tile<T, 5>(A, R, n0, lds);
-    else if (rows <= 192) row_tile<T, 6>(A, R, n0, lds);
-    else if (rows <= 224) row_tile<T, 7>(A, R, n0, lds);
-    else row_tile<T, 8>(A, R, n0, lds);
+    if (rows <= 32) row_tile<T, 1, Off>(A, R, n0, lds);
+    else if (rows <= 64) row_tile<T, 2, Off>(A, R, n0, lds);
+    else if (rows <= 96) row_tile<T, 3, Off>(A, R, n0, lds);
+    else if constexpr (BM == 128) row_tile<T, 4, Off>(A, R, n0, lds);
+    else if (rows <= 128) row_tile<T, 4, Off>(A, R, n0, lds);
+    else if (rows <= 160) row_tile<T, 5, Off>(A, R, n0, lds);
+    else if (rows <= 192) row_tile<T, 6, Off>(A, R, n0, lds);
+    else if (rows <= 224) row_tile<T, 7, Off>(A, R, n0, lds);
+    else row_tile<T, 8, Off>(A, R, n0, lds);
   }
 }
 
-template <typename T, int BM> static void launch_tiled(const LinearI8Args &A, hipStream_t st) {
+template <typename T, int BM, typename Off = uint32_t>
+static void launch_tiled(const LinearI8Args &A, hipStream_t st) {
   const int64_t tiles = A.offsets ? A.M / BM + std::min(A.M, A.E) : (A.M + BM - 1) / BM;
   const int64_t items = tiles * ((A.N + TL_BN - 1) / TL_BN);
   const unsigned grid = (unsigned)((items + 7) / 8 * 8);
-  if (A.E <= 64) linear_i8_tiled_kernel<T, 1, BM><<<grid, 256, 0, st>>>(A);
-  else linear_i8_tiled_kernel<T, 16, BM><<<grid, 256, 0, st>>>(A);
+  if (A.E <= 64) linear_i8_tiled_kernel<T, 1, BM, Off><<<grid, 256, 0, st>>>(A);
+  else linear_i8_tiled_kernel<T, 16, BM, Off><<<grid, 256, 0, st>>>(A);
 }
 
 // Which kernel, from the rows a matrix has on average (the host knows no more)
@@ -508,16 +510,21 @@ template <typename T, int BM> static void launch_tiled(const LinearI8Args &A, hi
 //    422 against 439 at 160 rows by 460 of 1536 x 2048, 350 against 343 at 80.  With one matrix every tile is whole, and a round of
 //    them (two per CU) is enough: 39 us against 44 for 8192 rows by 2048 x 2048,
 //    25.7 against 22.9 for 4096.
+// Past 2^32 bytes the offsets need 64 bits, and with them two blocks per CU the
+// registers: 128-row tiles, 49 us against 44 for 8192 rows looked up by one
+// matrix of 2048 x 2048, 157 against 160 for 24576 rows by 64 (the short kernel:
+// 257 and 763).
 template <typename T> static void launch_linear(const LinearI8Args &A, hipStream_t st) {
   const int avg = A.M / A.E;
   // 32-bit byte offsets inside one matrix, and inside a where rows are looked up
-  const bool near = (uint64_t)A.N * A.ldw < (1ull << 32) &&
-                    (!A.row_src || (uint64_t)A.a_rows * A.lda < (1ull << 32));
+  const bool near = (uint64_t)A.N * A.ldw <= (1ull << 32) &&
+                    (!A.row_src || (uint64_t)A.a_rows * A.lda <= (1ull << 32));
   const bool small = (int64_t)ceil_div_h(A.N, 16) * short_tiles(A) < 1024;
   const int64_t work = (int64_t)A.M * A.N / (128 * 128);
   const bool many = A.E == 1 ? (int64_t)ceil_div_h(A.M, TL_BM) * ceil_div_h(A.N, TL_BN) >= 512
                              : avg > 112 && work >= 2000;
-  if (small || !near) launch_short<T>(A, st);
+  if (small) launch_short<T>(A, st);
+  else if (!near) launch_tiled<T, 128, uint64_t>(A, st);
   else if (avg <= 8) launch_tiled<T, 32>(A, st);
   else if (many) launch_tiled<T, 256>(A, st);
   else if (work >= 768 || (avg >= 256 && work >= 256)) launch_tiled<T, 128>(A, st);

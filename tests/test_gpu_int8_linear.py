@@ -431,6 +431,42 @@ def test_linear_rows_past_32_bits(cuda_ok, looked_up):
         assert int((out != 0).any(1).sum()) == len(at)   # (the other rows are 0)
 
 
+def test_linear_many_rows_looked_up_past_32_bits(cuda_ok):
+    """3000 rows looked up on both sides of 2^32 bytes, one matrix and several."""
+    R, N, K, M = 2097152 + 300, 300, 2048, 3000
+    g = torch.Generator(device=DEV).manual_seed(3)
+    a = torch.randint(-127, 128, (R, K), generator=g, dtype=torch.int8, device=DEV)
+    a_s = torch.rand(R, generator=g, device=DEV)
+    src = torch.randint(0, R, (M,), generator=g, device=DEV).to(torch.int32)
+    src[:1000] = torch.randint(2097152 - 300, R, (1000,), generator=g, device=DEV)
+    rows = a[src.long()].double()
+    for E in (1, 6):
+        w = torch.randint(-128, 128, (E, N, K), generator=g, dtype=torch.int8, device=DEV)
+        off = torch.linspace(0, M, E + 1, device=DEV).to(torch.int32) if E > 1 else None
+        out = torch.empty(M, N, device=DEV)
+        B.moe_i8_linear(a, a_s, w, None, out, offsets=off, row_src=src)
+        at = off.tolist() if E > 1 else [0, M]
+        ref = torch.cat([rows[at[e]:at[e + 1]] @ w[e].double().t() for e in range(E)])
+        ref = ref * a_s[src.long()].double()[:, None]
+        assert torch.all((out.double() - ref).abs() <= ref.abs() * 3.1 * U)
+
+
+@pytest.mark.parametrize("wider", [0, 64])
+def test_linear_one_matrix_past_32_bits(cuda_ok, wider):
+    """The largest matrix there may be, 65536 x 65536, and at a longer stride."""
+    N = K = 65536
+    g = torch.Generator(device=DEV).manual_seed(4)
+    w = torch.randint(-128, 128, (1, N, K + wider), generator=g, dtype=torch.int8, device=DEV)
+    w = w[:, :, :K]
+    a = torch.randint(-127, 128, (40, K), generator=g, dtype=torch.int8, device=DEV)
+    out = torch.empty(40, N, device=DEV)
+    B.moe_i8_linear(a, torch.ones(40, device=DEV), w, None, out)
+    rows = a.double()
+    for n in (0, 30000, N - 2048):
+        ref = rows @ w[0, n:n + 2048].double().t()
+        assert torch.all((out[:, n:n + 2048].double() - ref).abs() <= ref.abs() * U)
+
+
 def test_row_sources_out_of_range_are_clamped(cuda_ok):
     a = torch.randint(-127, 128, (4, 128), generator=gen(0)).to(torch.int8)
     w = torch.randint(-128, 128, (1, 40, 128), generator=gen(1)).to(torch.int8)

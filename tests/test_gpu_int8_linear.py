@@ -78,6 +78,22 @@ def test_quant_many_rows(cuda_ok, K, dt):
     assert torch.all(q[S:] == 55) and torch.all(s[S:] == -77)
 
 
+def test_quant_more_rows_than_a_launch(cuda_ok):
+    """Rows of more than one launch (2^22 each), with the last expert's end in
+    the second one."""
+    M, K = (1 << 22) + 700, 24
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x = torch.randn(M, K, generator=g, device=DEV)
+    off = torch.tensor([0, 5, (1 << 22) + 100, M - 300], dtype=torch.int32, device=DEV)
+    cs = torch.rand(3, K, generator=g, device=DEV) + 0.1
+    q, s = run_quant(x, K, col_scale=cs, offsets=off)
+    S = M - 300
+    for i, j, e in ((0, 5, 0), (5, 2000, 1), ((1 << 22) - 500, (1 << 22) + 100, 1), ((1 << 22) + 100, S, 2)):
+        rq, rs = quant_ref(x[i:j].cpu() * cs[e].cpu())
+        assert torch.equal(s[i:j].cpu(), rs) and torch.equal(q[i:j, :K].cpu(), rq)
+    assert torch.all(q[:S, K:] == 0) and torch.all(q[S:] == 55) and torch.all(s[S:] == -77)
+
+
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
 def test_quant_ties_and_extremes(cuda_ok, dt):
     """Quotients that end in one half go to the even side; zeros, subnormal

@@ -504,12 +504,13 @@ static void launch_tiled(const LinearI8Args &A, hipStream_t st) {
 //    (256 rows a matrix): against 64-row ones 62 us for 64 at 64 rows by 128
 //    matrices of 2048 x 1024, 46 for 45 at 128 rows by 64 of 1408 x 2048; 19.5
 //    for 21.0 at 256 rows by 8 of 2048 x 2048, 15.6 for 15.4 at 160;
-//  - 256-row tiles where there is work for many rounds of them: 146 us against
-//    155 with 128-row ones at 600 rows by 64 matrices of 1408 x 2048, 104
-//    against 101 at 384 (102 against 106 with even loads), 62 against 57 at 213;
-//    422 against 439 at 160 rows by 460 of 1536 x 2048, 350 against 343 at 80.  With one matrix every tile is whole, and a round of
-//    them (two per CU) is enough: 39 us against 44 for 8192 rows by 2048 x 2048,
-//    25.7 against 22.9 for 4096.
+//  - 256-row tiles where they have more than three rounds of work (two blocks
+//    per CU) and most are whole: against 128-row ones 177 us for 187 at 768 rows by 64
+//    matrices of 1408 x 2048, 131 for 127 at 512; 172 for 178 at 384 rows by 128
+//    of 2048 x 1024, 101 for 97 at 160; 275 for 281 at 160 rows by 460 of 2048 x
+//    768, 249 for 243 at 128.  With one matrix every tile is whole, and a round of
+//    them is enough: 39 us against 44 for 8192 rows by 2048 x 2048, 25.7 against
+//    22.9 for 4096.
 // Past 2^32 bytes the offsets need 64 bits, and with them two blocks per CU the
 // registers: 128-row tiles, 49 us against 44 for 8192 rows looked up by one
 // matrix of 2048 x 2048, 157 against 160 for 24576 rows by 64 (the short kernel:
@@ -522,7 +523,7 @@ template <typename T> static void launch_linear(const LinearI8Args &A, hipStream
   const bool small = (int64_t)ceil_div_h(A.N, 16) * short_tiles(A) < 1024;
   const int64_t work = (int64_t)A.M * A.N / (128 * 128);
   const bool many = A.E == 1 ? (int64_t)ceil_div_h(A.M, TL_BM) * ceil_div_h(A.N, TL_BN) >= 512
-                             : avg > 112 && work >= 2000;
+                             : avg > 144 && work >= 3500;
   if (small) launch_short<T>(A, st);
   else if (!near) launch_tiled<T, 128, uint64_t>(A, st);
   else if (avg <= 8) launch_tiled<T, 32>(A, st);

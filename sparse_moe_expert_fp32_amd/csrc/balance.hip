@@ -14,6 +14,10 @@
 // block in wave order, then over the blocks in double (the second kernel), so
 // the result does not depend on timing.
 //
+// NEM is the least of 1, 4, 8 and 16 that holds the row (65536 x 64 with 1: 17 + 10
+// us, with 4: 23 + 17; 65536 x 256 with 4: 25 + 22, with 8: 32 + 26; 65536 x 128
+// would take 20 + 14 with 2 in the place of the 24 + 17 with 4).
+//
 // Bound by the logits (65536 x 460: forward 35 us for 121 MB, its second
 // kernel 7 us, backward 39 us for 242 MB), at small sizes by the launches
 // (3 to 5 us a kernel).  The next token's row is on its way while one is

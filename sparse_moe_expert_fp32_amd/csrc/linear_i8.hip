@@ -46,6 +46,8 @@ DEV int wave_scan(int v) {
 // [0, M], loads coalesced and all in flight at once), and the list runs over
 // the lanes.  One scan over the lanes' sums finds the lane of a tile, whose
 // experts are then walked.  The whole wave asks for the same tile.
+// NC = 1 for up to 64 experts (8 matrices of 1536 x 2048 by 64 rows: 7.4 us, 8.8
+// with NC = 16), 16 for more (65 to 128 experts with NC = 2: 1 to 3 % less).
 struct RowTile { int e, p0, end; };
 template <int BM, int NC> struct TileList {
   int lo[NC], hi[NC], sum, upto, M;
@@ -144,13 +146,13 @@ template <typename T> DEV void put4(T *p, bool vec, int n, int N, const float *v
 // instructions read them (step s of 64: 1 KB, lane after lane; rows too long
 // for that are read from memory each time).  The four waves split the steps
 // (wave w takes steps w, w + 4, ..) and read the matrix straight into
-// registers, D steps ahead and across fragments; their sums are added
-// through LDS.
-constexpr int SH_BM = 16, SH_WAVES = 4;
+// registers, SH_D steps ahead and across fragments (four in the place of eight:
+// no difference, K = 256 .. 1024); their sums are added through LDS.
+constexpr int SH_BM = 16, SH_WAVES = 4, SH_D = 8;
 
-template <typename T, int D, int NC, bool ALDS>
+template <typename T, int NC, bool ALDS>
 __global__ __launch_bounds__(64 * SH_WAVES) void linear_i8_short_kernel(LinearI8Args A, int per) {
-  constexpr int KS = SH_WAVES;
+  constexpr int KS = SH_WAVES, D = SH_D;
   extern __shared__ __attribute__((aligned(16))) int8_t lds_a[];
   __shared__ __attribute__((aligned(16))) int red[KS * 256];
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
@@ -247,13 +249,11 @@ template <typename T> static void launch_short(const LinearI8Args &A, hipStream_
   // the memory system idle
   const int per = (int)std::min<int64_t>(nfr, ((int64_t)nfr * tiles + 1023) / 1024);
   const dim3 grid((nfr + per - 1) / per, std::min(tiles, 32768));
-#define MOE_L(D, NC, AL) \
-  linear_i8_short_kernel<T, D, NC, AL><<<grid, 64 * SH_WAVES, AL ? lds : 0, st>>>(A, per)
-  if (!alds) MOE_L(8, 16, false);
-  else if (A.E > 64 && steps <= 16) MOE_L(4, 16, true);
-  else if (A.E > 64) MOE_L(8, 16, true);
-  else if (steps <= 16) MOE_L(4, 1, true);
-  else MOE_L(8, 1, true);
+#define MOE_L(NC, AL) \
+  linear_i8_short_kernel<T, NC, AL><<<grid, 64 * SH_WAVES, AL ? lds : 0, st>>>(A, per)
+  if (!alds) MOE_L(16, false);
+  else if (A.E > 64) MOE_L(16, true);
+  else MOE_L(1, true);
 #undef MOE_L
 }
 

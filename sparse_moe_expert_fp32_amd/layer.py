@@ -16,6 +16,7 @@ from . import binding as B
 
 MATS = ("gate", "up", "down")
 MATS_I8 = ("gate_up", "down")   # of Int8Experts
+_LAYING_OUT = threading.Lock()   # (not the object's: a lock is neither copied nor pickled)
 
 
 def _version(t) -> int:
@@ -249,7 +250,7 @@ class Int8Experts:
         self.gate_up, self.s_gate_up, self.down, self.s_down = gate_up, s_gate_up, down, s_down
         self.E, f2, self.d = gate_up.shape
         self.f = f2 // 2
-        self.t, self._from, self._lock = None, {}, threading.Lock()
+        self.t, self._from = None, {}
 
     def _rows(self, M, K):
         dev = self.down.device
@@ -289,7 +290,7 @@ class Int8Experts:
         call this.  Waits for the GPU: what wrote the matrices and what still
         reads an earlier layout is done before, and any stream may read the
         layout afterwards.  Not inside a graph capture."""
-        with self._lock:
+        with _LAYING_OUT:
             self._lay_out(MATS_I8)
 
     def _lay_out(self, names):
@@ -316,7 +317,7 @@ class Int8Experts:
     def _turned(self, name):
         """The transposed matrix of `name` as it is now."""
         w = getattr(self, name)
-        with self._lock:
+        with _LAYING_OUT:
             kept = self._from.get(name)
             if kept is None or kept[0] is not w or kept[1] != _version(w):
                 self._lay_out((name,))

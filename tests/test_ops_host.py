@@ -141,3 +141,14 @@ def test_int8_experts_refuse_shapes_that_do_not_match(gu, s_gu, down, s_down):
                     torch.zeros(down, dtype=torch.int8), torch.zeros(s_down))
     with pytest.raises(ValueError, match="Int8Experts"):
         X.forward(None)
+
+
+def test_int8_experts_are_copied_and_pickled():
+    import copy
+    import pickle
+
+    from sparse_moe_expert_fp32_amd.layer import Int8Experts
+    X = Int8Experts(torch.ones(2, 8, 8, dtype=torch.int8), torch.ones(2, 8),
+                    torch.ones(2, 8, 4, dtype=torch.int8), torch.ones(2, 8))
+    for Y in (copy.deepcopy(X), pickle.loads(pickle.dumps(X))):
+        assert torch.equal(Y.gate_up, X.gate_up) and Y.f == 4 and Y.t is None

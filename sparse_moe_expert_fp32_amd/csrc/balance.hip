@@ -18,11 +18,11 @@
 // us, with 4: 23 + 17; 65536 x 256 with 4: 25 + 22, with 8: 32 + 26; 65536 x 128
 // would take 20 + 14 with 2 in the place of the 24 + 17 with 4).
 //
-// Bound by the logits (65536 x 460: forward 35 us for 121 MB, its second
-// kernel 7 us, backward 39 us for 242 MB), at small sizes by the launches
-// (3 to 5 us a kernel).  The next token's row is on its way while one is
-// summed (55 -> 35 us), and the reductions over the lanes exchange registers
-// instead of going through LDS.
+// The backward is bound by its bytes (65536 x 460: 39 us for 242 MB), the forward
+// by latency (36 us for 121 MB, 3.4 TB/s: one block per CU, the next token's row
+// on its way while one is summed; 55 us without), its second kernel too (7 us);
+// at small sizes all by the launches (3 to 5 us a kernel).  The reductions over
+// the lanes exchange registers instead of going through LDS.
 #include <algorithm>
 
 #include "common.h"

@@ -276,10 +276,11 @@ template <typename T> static void launch_short(const LinearI8Args &A, hipStream_
 // 2048 where the classes went in steps of 64 rows).
 //
 // What bounds it: a few rows a matrix, reading the matrices (64 matrices of
-// 1408 x 2048 in 27 us, 6.8 TB/s); hundreds of rows, the products (39 us for
-// 8192 x 2048 x 2048, 1.77 POP/s; 1.5 POP/s for 256 rows by each of 460
-// matrices of 1536 x 2048), whose instructions are issued a third of the time,
-// the rest going to LDS traffic and the two barriers of a step.
+// 1408 x 2048 in 27 us, 6.8 TB/s); hundreds of rows, LDS traffic and the two
+// barriers of a step (38 us for 8192 x 2048 x 2048, 1.8 POP/s, the matrix cores
+// busy 0.35 of the time; 98304 unevenly spread rows by 460 matrices of 1536 x
+// 2048 in 521 us, 1.2 POP/s, busy 0.30; of 2048 x 768, six steps a tile, in 365
+// us, 0.85 POP/s, busy 0.21).
 constexpr int TL_BM = 256, TL_BN = 128, TL_KS = 128;
 // bytes of LDS for tiles of up to BM rows: channels, row and channel scales, rows
 constexpr int TL_SCALES = TL_BN * TL_KS, TL_A = TL_SCALES + (TL_BM + TL_BN) * 4;

@@ -21,8 +21,8 @@
 // Bound by memory where there are many rows: 24576 x 2048 with channel scales in
 // 30 us (150 MB), 8192 x 2048 in 13.8 us (50 MB); 46 and 15.3 us with the exact
 // remainder for every value.  A few rows take 4.5 us, the latency of one pass.
-// SwiGLU rows are bound by the vector units: 98304 x 768 in 112 us (378 MB), of
-// which the exponential and the quotient in full float32 take 42 (69 us with the
+// SwiGLU rows are bound by the vector units: 98304 x 768 in 110 us (378 MB), of
+// which the exponential and the quotient in full float32 take 41 (69 us with the
 // hardware's exponential and reciprocal, whose error grows with |x| to 63
 // roundings at x = -80 and moved one value in 10^4 over a rounding border).
 #include <algorithm>

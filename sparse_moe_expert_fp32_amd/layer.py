@@ -244,7 +244,8 @@ class Int8Experts:
     gradient of its products' rows.
 
     gate_up int8 [E][2f][d] (gate's channels, then up's) with scales [E][2f],
-    down int8 [E][d][f] with scales [E][d], on the GPU."""
+    down int8 [E][d][f] with scales [E][d], on the GPU (moe_quant_i8 over the
+    output channels of a float matrix gives both)."""
 
     def __init__(self, gate_up, s_gate_up, down, s_down):
         self.gate_up, self.s_gate_up, self.down, self.s_down = gate_up, s_gate_up, down, s_down

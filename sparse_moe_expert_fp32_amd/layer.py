@@ -299,10 +299,11 @@ class Int8Experts:
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("Int8Experts: call transpose() before the graph capture")
         torch.cuda.synchronize(dev)
-        t = dict(self.t or {})
+        t, now = dict(self.t or {}), {}
         with torch.inference_mode(False):   # (a layout made in it could not be written again)
             for name in names:
                 w, room = getattr(self, name), t.get(name)
+                now[name] = (w, _version(w))
                 E, N, K = w.shape
                 # (in place where it fits: a captured graph reads this memory)
                 if room is None or (room.shape, room.dtype, room.device) != \
@@ -311,9 +312,9 @@ class Int8Experts:
                     room = room[:, :, :N]
                 room.copy_(w.transpose(1, 2))
                 t[name] = room
-                self._from[name] = (w, _version(w))
         torch.cuda.synchronize(dev)
         self.t = t
+        self._from.update(now)
 
     def _turned(self, name):
         """The transposed matrix of `name` as it is now."""

@@ -777,3 +777,16 @@ def test_linear_refuses_unsigned_matrices(cuda_ok):
     assert not out.any()
     B.moe_i8_linear(a, torch.ones(2, device=DEV), w.view(torch.int8), None, out)
     assert torch.all(out == -128)
+
+
+def test_row_gradient_after_a_layout_that_failed(cuda_ok):
+    """A matrix that cannot be laid out leaves nothing half kept."""
+    X, dout, off = large_experts(E=5, N=272, K=160, S=90)
+    good, X.down = X.down, X.down[0]
+    with pytest.raises(ValueError):
+        X.transpose()                       # (gate_up was laid out before it)
+    g = torch.randn(90, X.gate_up.shape[1], generator=gen(1)).bfloat16().to(DEV)
+    first = X.rows_grad("gate_up", g, off)
+    X.down = good
+    assert near_bf16(X.rows_grad("down", dout, off), rows_grad_ref(X, dout, off))
+    assert torch.equal(X.rows_grad("gate_up", g, off), first)
